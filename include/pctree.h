@@ -10,6 +10,12 @@
  *   tree_ancestor_mask  self-plus-ancestor bitmask for tree attention
  *   tree_verify_accept  greedy verification: argmax, accept walk, correction
  *   pct_score_parents   one depth of PCTree's batched parent scoring
+ * and around the target's forward pass, over a paged key-value cache:
+ *   kv_pages_resize     block tables grown and shrunk to the requests' lengths
+ *   kv_tree_slots       cache slots and positions of the tree's nodes
+ *   kv_append           the nodes' new K and V rows into their slots
+ *   tree_attention      attention of the nodes over the cache (decode: one node)
+ *   kv_commit           accepted nodes' K and V rows moved behind the context
  *
  * Conventions shared by every call
  * --------------------------------
@@ -71,7 +77,11 @@ enum {
   PCT_DEV_BAD_COUNT = 4,      /* count outside [1, n_stride]                                  */
   PCT_DEV_DEPTH_OVERFLOW = 8, /* accept walk longer than max_depth                            */
   PCT_DEV_BAD_COST = 16,      /* CaDDTree cost C(n) <= 0 for some n in [1, n_max]             */
-  PCT_DEV_TIMEOUT = 32        /* a bounded device wait gave up                                */
+  PCT_DEV_TIMEOUT = 32,       /* a bounded device wait gave up                                */
+  PCT_DEV_BAD_PAGE = 64,      /* a block-table entry, slot or free page outside the cache     */
+  PCT_DEV_NO_PAGE = 128,      /* the free list has too few pages left for this request        */
+  PCT_DEV_BAD_LENGTH = 256,   /* a length below 0 or beyond the block table's columns         */
+  PCT_DEV_BAD_PATH = 512      /* an accepted path that does not rise within [1, count)        */
 };
 
 /* ------------------------------------------------------------------------ *
@@ -362,6 +372,149 @@ int32_t tree_verify_accept_noalloc(int32_t batch, int32_t n_stride, int32_t voca
                                    const int32_t* count, const void* target, int32_t target_dtype,
                                    int32_t* argmax, int32_t* accept_len, int32_t* accept_path,
                                    int32_t* correction, int32_t* dev_status, void* cuda_stream);
+
+/* ------------------------------------------------------------------------ *
+ * Paged key-value cache.
+ * A cache holds n_pages pages of page_size tokens; token t of request b lies
+ * in page block_table[b][t / page_size] at place t % page_size, and slot
+ * s = page * page_size + place names it in the whole cache. Request b has
+ * ctx_len[b] tokens in the cache; a round's tree adds node i (0 = the root,
+ * the last accepted token, whose K and V are not in the cache yet) as token
+ * ctx_len[b] + i. One block table serves every layer.
+ * K and V caches of one layer are [n_pages][page_size][heads_kv][head_dim]
+ * with any strides (elements, innermost contiguous; the same for K and V), so
+ * [n_pages][heads_kv][page_size][head_dim] and K and V interleaved by page work
+ * too. Strides are multiples of 16 bytes, pointers 16-byte aligned (else
+ * PCT_EINVAL); head_dim is a multiple of 8 in 8..256. Offsets are 64-bit.
+ * Block tables are [batch][max_pages] int32; entries past a request's pages are
+ * never read. A request uses a page at most once, no two requests write the
+ * same page, and the calls do not check that.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t n_pages;      /* pages of the cache, >= 1                                  */
+  int32_t page_size;    /* tokens per page, 1..65536                                 */
+  int32_t max_pages;    /* columns of the block table, >= 1;
+                           max_pages * page_size <= 2^30                             */
+  int32_t heads_kv;     /* 1..1024                                                   */
+  int32_t head_dim;     /* 8..256, a multiple of 8                                   */
+  int32_t dtype;        /* PCT_F32 or PCT_BF16                                       */
+  int64_t page_stride;  /* elements between pages                                    */
+  int64_t slot_stride;  /* elements between the places of a page                     */
+  int64_t head_stride;  /* elements between heads                                    */
+} kv_cache_desc;
+
+/* Block tables to the requests' lengths, pages from and to one free list.
+ * Request b is to hold want = ceil((ctx_len[b] + count[b]) / page_size) pages
+ * (count NULL: 0 for all).
+ *   - First every request with held[b] > want returns its pages from column want
+ *     on (entries become -1): in request and column order, the last page
+ *     returned ends up deepest, so that growing and shrinking back restores the
+ *     free list.
+ *   - Then, in request order, each request with held[b] < want takes the missing
+ *     pages from the top of the free list, column by column. The first request
+ *     that the list cannot serve, and every one after it that needs pages, takes
+ *     none: PCT_DEV_NO_PAGE, its row unchanged.
+ *   ctx_len [batch] int64, count [batch] int32 or NULL
+ *   block_table [batch][max_pages], held [batch]  int32, updated
+ *   free_pages [n_pages] int32, free_count [1] int32, updated: the list is
+ *     free_pages[0 .. free_count - 1], its top the last entry
+ *   dev_status [batch]: PCT_DEV_BAD_LENGTH (negative, or want or held outside
+ *     0..max_pages), PCT_DEV_BAD_PAGE (an entry to return outside the cache),
+ *     PCT_DEV_BAD_COUNT (every request: free_count outside 0..n_pages, or the
+ *     returns do not fit the list); such a request's row stays as it was.
+ * A page taken from the list that is outside the cache goes into the table as it
+ * is (the calls that use it report it). One launch, no workspace. */
+int32_t kv_pages_resize(int32_t batch, int32_t page_size, int32_t max_pages, int32_t n_pages,
+                        const int64_t* ctx_len, const int32_t* count, int32_t* block_table,
+                        int32_t* held, int32_t* free_pages, int32_t* free_count,
+                        int32_t* dev_status, void* cuda_stream);
+
+/* Slots and positions of the tokens after the context.
+ *   slot [batch][n_stride] int64: block_table[b][t / page_size] * page_size +
+ *     t % page_size with t = ctx_len[b] + i; -1 at i >= count[b] and where the
+ *     table's entry is outside the cache (PCT_DEV_BAD_PAGE)
+ *   pos  [batch][n_stride] int64: ctx_len[b] + depth[b][i], the position a
+ *     rotary embedding takes (siblings share one); depth NULL: ctx_len[b] + i;
+ *     -1 at i >= count[b]
+ *   depth [batch][n_stride] int32 or NULL (a chain)
+ *   dev_status [batch]: PCT_DEV_BAD_COUNT (count outside 0..n_stride) and
+ *     PCT_DEV_BAD_LENGTH (ctx_len + count outside the table): both rows are -1.
+ * n_stride in 1..2^20. One launch, no workspace. */
+int32_t kv_tree_slots(int32_t batch, int32_t n_stride, int32_t page_size, int32_t max_pages,
+                      int32_t n_pages, const int64_t* ctx_len, const int32_t* count,
+                      const int32_t* depth, const int32_t* block_table, int64_t* slot,
+                      int64_t* pos, int32_t* dev_status, void* cuda_stream);
+
+/* K and V rows of new tokens into their slots.
+ *   k_new, v_new [batch][n_stride][heads_kv][head_dim] with the strides
+ *     new_stride = {request, token, head} (elements; the same for both; multiples
+ *     of 16 bytes), e.g. slices of a fused projection's output
+ *   slot [batch][n_stride] int64; a row with a negative slot is skipped, one past
+ *     the cache is skipped and sets PCT_DEV_BAD_PAGE. Rows of one call name
+ *     distinct slots; of two that name the same one either may remain, also in parts.
+ *   k_cache, v_cache: written at the slots; nothing else of them changes.
+ * new rows may not overlap the cache. desc->max_pages is not used. One launch. */
+int32_t kv_append(const kv_cache_desc* desc, int32_t batch, int32_t n_stride, const void* k_new,
+                  const void* v_new, const int64_t* new_stride, const int64_t* slot,
+                  void* k_cache, void* v_cache, int32_t* dev_status, void* cuda_stream);
+
+/* ------------------------------------------------------------------------ *
+ * Attention of a tree's nodes over the paged cache (tree attention).
+ * Row (b, i, h), i < count[b], with kv head h / (heads_q / heads_kv), sees token
+ * t < ctx_len[b], and node j (token ctx_len[b] + j) when j <= i and bit j of
+ * mask row i is set (the layout tree_ancestor_mask writes; bits at j > i are not
+ * read); with mask NULL, every j <= i (a causal chain: a decode step with
+ * n_stride = 1, a prompt's chunk). The nodes' K and V are in the cache already.
+ *   s_t = scale * <q, k_t>,  out = sum_t softmax(s)_t v_t,  lse = ln sum_t exp(s_t)
+ * A row that sees no token, and every row at i >= count[b], gives out = 0 and
+ * lse = -inf. Cache places at or past token ctx_len + count, and nodes a row
+ * does not see, do not enter its result whatever K holds there; V of the nodes
+ * below count must be finite (0 * inf is NaN).
+ *   q   [batch][n_stride][heads_q][head_dim] with strides q_stride (elements,
+ *       {request, token, head}; multiples of 16 bytes), dtype of the cache
+ *   out [batch][n_stride][heads_q][head_dim], dense, dtype of the cache
+ *   lse [batch][n_stride][heads_q] float, or NULL
+ *   count [batch] int32, 0..n_stride, or NULL: n_stride for all
+ *   mask [batch][n_stride][ceil(n_stride / 32)] uint32 or NULL
+ *   dev_status [batch]: PCT_DEV_BAD_COUNT, PCT_DEV_BAD_LENGTH (ctx_len negative or
+ *     ctx_len + count beyond the table): the request's rows are 0 and -inf;
+ *     PCT_DEV_BAD_PAGE: tokens of that page are left out; PCT_DEV_TIMEOUT: the
+ *     request's rows are unspecified.
+ * bf16: products on the tensor cores with fp32 accumulation; the softmax's
+ * weights are rounded to bf16 for the second product, their sum is not. Scores,
+ * maxima, sums and the joins of a split axis are fp32. Results are the same from
+ * call to call on the same device.
+ * heads_q is a multiple of heads_kv, at most 64 times it; n_stride in 1..65536;
+ * scale finite. The work is cut into equal parts over the device, along the cache
+ * where rows are few, and joined by a second launch.
+ * ------------------------------------------------------------------------ */
+size_t tree_attention_workspace(const kv_cache_desc* desc, int32_t batch, int32_t n_stride,
+                                int32_t heads_q);
+int32_t tree_attention(const kv_cache_desc* desc, int32_t batch, int32_t n_stride,
+                       int32_t heads_q, float scale, const void* q, const int64_t* q_stride,
+                       const void* k_cache, const void* v_cache, const int32_t* block_table,
+                       const int64_t* ctx_len, const int32_t* count, const uint32_t* mask,
+                       void* out, float* lse, int32_t* dev_status, void* workspace,
+                       size_t ws_bytes, void* cuda_stream);
+
+/* After the accept walk: node accept_path[b][i], i < accept_len[b], moves to
+ * token ctx_len[b] + 1 + i in K and V of every layer (the root stays at token
+ * ctx_len[b]), and new_len[b] = ctx_len[b] + 1 + accept_len[b]. accept_len and
+ * accept_path are what tree_verify_accept and tree_verify_walk write: the path
+ * rises strictly. What lay behind the new length is unspecified afterwards.
+ *   k_cache, v_cache: layer l at l * layer_stride elements (a multiple of 16 bytes)
+ *   accept_path [batch][max_depth] int32
+ *   new_len [batch] int64, not overlapping ctx_len
+ *   dev_status [batch]: PCT_DEV_BAD_COUNT (count below 1), PCT_DEV_BAD_LENGTH,
+ *     PCT_DEV_BAD_PATH (accept_len outside 0..max_depth, or the path does not rise
+ *     strictly within [1, count)), PCT_DEV_BAD_PAGE: the request's cache rows stay
+ *     as they were and new_len[b] = ctx_len[b].
+ * layers in 1..65535, max_depth in 1..4096. One launch, no workspace. */
+int32_t kv_commit(const kv_cache_desc* desc, int32_t batch, int32_t layers, int64_t layer_stride,
+                  int32_t max_depth, void* k_cache, void* v_cache, const int32_t* block_table,
+                  const int64_t* ctx_len, const int32_t* count, const int32_t* accept_len,
+                  const int32_t* accept_path, int64_t* new_len, int32_t* dev_status,
+                  void* cuda_stream);
 
 /* ------------------------------------------------------------------------ *
  * Kernel trace (off by default; host-side bookkeeping only). While on, every

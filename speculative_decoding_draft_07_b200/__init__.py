@@ -22,6 +22,12 @@ missing:
 * ``pct_score_parents``  -- one depth of PCTree's batched parent scoring.
 * ``cadd_cost_fit``      -- the non-negative fit of CaDDTree's verification cost
   C_v(n; l) = a + b l + c n + e n^2 to latency samples, on the device.
+* ``kv_pages_resize``, ``kv_tree_slots`` -- block tables of a paged key-value cache
+  from request lengths, and the tree nodes' cache slots and positions.
+* ``kv_append``          -- the nodes' new K and V rows into their slots.
+* ``tree_attention``     -- attention of the nodes over the paged cache with the
+  ancestor bitmask (causal without it); one node a request is the decode step.
+* ``kv_commit``          -- the accepted path's K and V rows moved behind the context.
 * ``budget.ddtree_grow`` -- the fixed-budget best-first tree (CaDDTree's growth
   with the stop disabled), a call of ``cadd_tree_grow``.
 
@@ -36,7 +42,9 @@ from ._lib import (  # noqa: F401
     BuildDesc, CaddDesc, PctError, TreeOut, VerifyOut, LIB_PATH, EXPORTED,
     PCT_OK, PCT_EINVAL, PCT_EWORKSPACE, PCT_ECUDA, PCT_EDEVICE, PCT_ETIMEOUT, PCT_EUNSUPPORTED,
     PCT_F32, PCT_BF16, DEV_BAD_PARENT, DEV_BAD_TOKEN, DEV_BAD_COUNT, DEV_DEPTH_OVERFLOW,
-    DEV_BAD_COST, DEV_TIMEOUT,
+    DEV_BAD_COST, DEV_TIMEOUT, DEV_BAD_PAGE, DEV_NO_PAGE, DEV_BAD_LENGTH, DEV_BAD_PATH,
+    KvCacheDesc, AttnOut, kv_pages_resize, kv_tree_slots, kv_append, tree_attention,
+    tree_attention_workspace, kv_commit,
     lib, build_desc, cadd_desc, pct_tree_build_workspace, pct_tree_build, pct_score_parents,
     cadd_tree_grow, tree_ancestor_mask, tree_verify_accept, tree_verify_walk, tree_accept_sim,
     cadd_cost_fit, markov_transpose, trace_enable, trace_reset,

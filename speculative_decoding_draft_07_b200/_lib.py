@@ -7,6 +7,7 @@ missing it raises instead of falling back to anything else.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -21,6 +22,7 @@ PCT_OK, PCT_EINVAL, PCT_EWORKSPACE, PCT_ECUDA, PCT_EDEVICE, PCT_ETIMEOUT, PCT_EU
 PCT_F32, PCT_BF16 = 0, 1
 DEV_BAD_PARENT, DEV_BAD_TOKEN, DEV_BAD_COUNT, DEV_DEPTH_OVERFLOW, DEV_BAD_COST, DEV_TIMEOUT = (
     1, 2, 4, 8, 16, 32)
+DEV_BAD_PAGE, DEV_NO_PAGE, DEV_BAD_LENGTH, DEV_BAD_PATH = 64, 128, 256, 512
 _NAMES = {0: "PCT_OK", 1: "PCT_EINVAL", 2: "PCT_EWORKSPACE", 3: "PCT_ECUDA", 4: "PCT_EDEVICE",
           5: "PCT_ETIMEOUT", 6: "PCT_EUNSUPPORTED"}
 
@@ -31,7 +33,8 @@ EXPORTED = [
     "pct_trace_read", "pct_version", "tree_verify_accept_noalloc", "tree_verify_walk",
     "tree_accept_sim",
     "cadd_cost_fit", "pct_tree_build_seeded", "cadd_tree_grow_topk", "pct_markov_rank_pad",
-    "pct_markov_transpose",
+    "pct_markov_transpose", "kv_pages_resize", "kv_tree_slots", "kv_append",
+    "tree_attention_workspace", "tree_attention", "kv_commit",
 ]
 
 
@@ -55,6 +58,14 @@ class CaddDesc(ctypes.Structure):
                 ("c", ctypes.c_float), ("e", ctypes.c_float)]
 
 
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("heads_kv", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -69,6 +80,7 @@ def lib() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     bd, cd = ctypes.POINTER(BuildDesc), ctypes.POINTER(CaddDesc)
+    kd = ctypes.POINTER(KvCacheDesc)
     sig = {
         "pct_tree_build_workspace": (sz, [bd]),
         "pct_tree_build": (i32, [bd, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
@@ -96,6 +108,14 @@ def lib() -> ctypes.CDLL:
         "pct_markov_transpose": (i32, [i32, i32, vp, vp, vp]),
         "cadd_tree_grow_topk": (i32, [cd, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                       sz, vp]),
+        "kv_pages_resize": (i32, [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "kv_tree_slots": (i32, [i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "kv_append": (i32, [kd, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "tree_attention_workspace": (sz, [kd, i32, i32, i32]),
+        "tree_attention": (i32, [kd, i32, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp,
+                                 vp, vp, vp, vp, sz, vp]),
+        "kv_commit": (i32, [kd, i32, i32, ctypes.c_int64, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                            vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -411,6 +431,269 @@ def cadd_cost_fit(n: torch.Tensor, ell: torch.Tensor, lat: torch.Tensor, stream=
     code = lib().cadd_cost_fit(m, _p(n), _p(ell), _p(lat), _p(out), _p(status), _stream(stream))
     _raise(code, "cadd_cost_fit")
     return out, status
+
+
+# ---------------------------------------------------------------------------
+# Paged key-value cache. Unlike the calls above, these take strided views where
+# the ABI does, make the tensors' device current for the call when it is not,
+# and allocate their outputs and workspace on the stream they run on.
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _on(t: torch.Tensor, name: str, stream):
+    """(stream handle, context to allocate and launch in) for work on t's device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name} is on {dev}, expected a CUDA device")
+    if stream is None:
+        s = torch.cuda.current_stream(dev)
+        if dev.index == torch.cuda.current_device():
+            return s.cuda_stream, _HERE_ALREADY
+    else:
+        s = stream
+        if s.device != dev:
+            raise ValueError(f"stream is on {s.device}, {name} on {dev}")
+    return s.cuda_stream, torch.cuda.stream(s)
+
+
+def _strides(t: torch.Tensor, name: str, dev, shape, dtype=None):
+    """The element strides of all but the last axis of a view whose last axis is
+    contiguous (0 for an axis of one entry, which is never stepped over)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    return [0 if n == 1 else x for n, x in zip(t.shape[:-1], st[:-1])]
+
+
+def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, max_pages: int, layered: bool = False):
+    """(descriptor, layer stride) of K and V caches [layers][n_pages][page_size][heads][head_dim]
+    (no layer axis unless `layered`)."""
+    dims = 5 if layered else 4
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != dims:
+        raise ValueError("k_cache must be a %d-dimensional tensor" % dims)
+    st = _strides(k_cache, "k_cache", k_cache.device, k_cache.shape)
+    if _strides(v_cache, "v_cache", k_cache.device, k_cache.shape, k_cache.dtype) != st:
+        raise ValueError("k_cache and v_cache must have the same strides")
+    n_pages, page_size, heads, d = k_cache.shape[-4:]
+    return (KvCacheDesc(n_pages, page_size, max_pages, heads, d, _code(k_cache), *st[-3:]),
+            st[0] if layered else 0)
+
+
+def kv_pages_resize(ctx_len: torch.Tensor, block_table: torch.Tensor, held: torch.Tensor,
+                    free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int,
+                    count: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """Block tables [batch][max_pages] int32 grown and shrunk in place to
+    ceil((ctx_len + count) / page_size) pages a request, with pages from and back to
+    free_pages[:free_count] (int32 [n_pages] and [1]); held [batch] int32 counts each
+    request's pages. ctx_len [batch] int64, count [batch] int32. Returns status [batch]."""
+    s, ctx = _on(block_table, "block_table", stream)
+    dev = block_table.device
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch][max_pages]")
+    batch, max_pages = block_table.shape
+    _check(block_table, "block_table", dev, dtype=torch.int32)
+    _check(ctx_len, "ctx_len", dev, (batch,), torch.int64)
+    _check(held, "held", dev, (batch,), torch.int32)
+    _check(free_pages, "free_pages", dev, dtype=torch.int32)
+    _check(free_count, "free_count", dev, (1,), torch.int32)
+    if count is not None:
+        _check(count, "count", dev, (batch,), torch.int32)
+    with ctx:
+        if status is None:
+            status = torch.empty(batch, dtype=torch.int32, device=dev)
+        else:
+            _check(status, "status", dev, (batch,), torch.int32)
+        code = lib().kv_pages_resize(batch, page_size, max_pages, free_pages.numel(), _p(ctx_len),
+                                     _p(count), _p(block_table), _p(held), _p(free_pages),
+                                     _p(free_count), _p(status), s)
+    _raise(code, "kv_pages_resize")
+    return status
+
+
+def kv_tree_slots(ctx_len: torch.Tensor, count: torch.Tensor, block_table: torch.Tensor,
+                  n_stride: int, page_size: int, n_pages: int,
+                  depth: Optional[torch.Tensor] = None, slot: Optional[torch.Tensor] = None,
+                  pos: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                  stream=None):
+    """(slot, pos, status): cache slots and positions [batch][n_stride] int64 of the
+    count[b] tokens after ctx_len[b]; depth [batch][n_stride] int32 (a tree's node
+    depths) makes siblings share a position, None is a chain."""
+    s, ctx = _on(block_table, "block_table", stream)
+    dev = block_table.device
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [batch][max_pages]")
+    batch, max_pages = block_table.shape
+    _check(block_table, "block_table", dev, dtype=torch.int32)
+    _check(ctx_len, "ctx_len", dev, (batch,), torch.int64)
+    _check(count, "count", dev, (batch,), torch.int32)
+    if depth is not None:
+        _check(depth, "depth", dev, (batch, n_stride), torch.int32)
+    with ctx:
+        if slot is None:
+            slot = torch.empty((batch, n_stride), dtype=torch.int64, device=dev)
+        else:
+            _check(slot, "slot", dev, (batch, n_stride), torch.int64)
+        if pos is None:
+            pos = torch.empty((batch, n_stride), dtype=torch.int64, device=dev)
+        else:
+            _check(pos, "pos", dev, (batch, n_stride), torch.int64)
+        if status is None:
+            status = torch.empty(batch, dtype=torch.int32, device=dev)
+        else:
+            _check(status, "status", dev, (batch,), torch.int32)
+        code = lib().kv_tree_slots(batch, n_stride, page_size, max_pages, n_pages, _p(ctx_len),
+                                   _p(count), _p(depth), _p(block_table), _p(slot), _p(pos),
+                                   _p(status), s)
+    _raise(code, "kv_tree_slots")
+    return slot, pos, status
+
+
+def kv_append(k_new: torch.Tensor, v_new: torch.Tensor, slot: torch.Tensor, k_cache: torch.Tensor,
+              v_cache: torch.Tensor, status: Optional[torch.Tensor] = None,
+              stream=None) -> torch.Tensor:
+    """Rows k_new, v_new [batch][n_stride][heads][head_dim] (views with a contiguous
+    last axis and equal strides) into the caches [n_pages][page_size][heads][head_dim] at
+    slot [batch][n_stride] int64 (negative: skipped). Returns status [batch]."""
+    s, ctx = _on(k_cache, "k_cache", stream)
+    dev = k_cache.device
+    desc, _ = _cache(k_cache, v_cache, 1)
+    if not isinstance(slot, torch.Tensor) or slot.dim() != 2:
+        raise ValueError("slot must be [batch][n_stride]")
+    batch, n = slot.shape
+    _check(slot, "slot", dev, dtype=torch.int64)
+    shape = (batch, n, desc.heads_kv, desc.head_dim)
+    st = _strides(k_new, "k_new", dev, shape, k_cache.dtype)
+    if _strides(v_new, "v_new", dev, shape, k_cache.dtype) != st:
+        raise ValueError("k_new and v_new must have the same strides")
+    with ctx:
+        if status is None:
+            status = torch.empty(batch, dtype=torch.int32, device=dev)
+        else:
+            _check(status, "status", dev, (batch,), torch.int32)
+        code = lib().kv_append(ctypes.byref(desc), batch, n, _p(k_new), _p(v_new),
+                               (ctypes.c_int64 * 3)(*st), _p(slot), _p(k_cache), _p(v_cache),
+                               _p(status), s)
+    _raise(code, "kv_append")
+    return status
+
+
+@dataclass
+class AttnOut:
+    out: torch.Tensor
+    lse: torch.Tensor
+    status: torch.Tensor
+
+
+def tree_attention_workspace(k_cache: torch.Tensor, v_cache: torch.Tensor, max_pages: int,
+                             batch: int, n_stride: int, heads_q: int) -> int:
+    """Workspace bytes tree_attention needs for these shapes on the current device."""
+    desc, _ = _cache(k_cache, v_cache, max_pages)
+    return int(lib().tree_attention_workspace(ctypes.byref(desc), batch, n_stride, heads_q))
+
+
+def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   block_table: torch.Tensor, ctx_len: torch.Tensor,
+                   count: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                   scale: Optional[float] = None, out: Optional[AttnOut] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> AttnOut:
+    """Attention of a tree's nodes over the paged cache. q [batch][n_stride][heads_q][head_dim]
+    (a view with a contiguous last axis), caches [n_pages][page_size][heads_kv][head_dim] that
+    hold the nodes' K and V as tokens ctx_len + i, block_table [batch][max_pages] int32,
+    ctx_len [batch] int64, count [batch] int32 (None: n_stride for all), mask the words of
+    tree_ancestor_mask [batch][n_stride][ceil(n_stride / 32)] int32 (None: a causal chain; a
+    decode step with n_stride = 1). scale defaults to head_dim ** -0.5. Rows at or past count
+    are 0, their lse -inf."""
+    s, ctx = _on(q, "q", stream)
+    dev = q.device
+    if q.dim() != 4:
+        raise ValueError("q must be [batch][n_stride][heads_q][head_dim]")
+    batch, n, hq, d = q.shape
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [batch][max_pages]")
+    max_pages = block_table.shape[1]
+    _check(block_table, "block_table", dev, (batch, max_pages), torch.int32)
+    desc, _ = _cache(k_cache, v_cache, max_pages)
+    if k_cache.device != dev:
+        raise ValueError(f"k_cache is on {k_cache.device}, expected {dev}")
+    st = _strides(q, "q", dev, (batch, n, hq, desc.head_dim), k_cache.dtype)
+    _check(ctx_len, "ctx_len", dev, (batch,), torch.int64)
+    if count is not None:
+        _check(count, "count", dev, (batch,), torch.int32)
+    if mask is not None:
+        _check(mask, "mask", dev, (batch, n, (n + 31) // 32), torch.int32)
+    with ctx:
+        if out is None:
+            out = AttnOut(torch.empty((batch, n, hq, d), dtype=q.dtype, device=dev),
+                          torch.empty((batch, n, hq), dtype=torch.float32, device=dev),
+                          torch.empty(batch, dtype=torch.int32, device=dev))
+        else:
+            _check(out.out, "out.out", dev, (batch, n, hq, d), q.dtype)
+            if out.lse is not None:
+                _check(out.lse, "out.lse", dev, (batch, n, hq), torch.float32)
+            _check(out.status, "out.status", dev, (batch,), torch.int32)
+        nbytes = int(lib().tree_attention_workspace(ctypes.byref(desc), batch, n, hq))
+        if nbytes == 0:
+            _raise(PCT_EINVAL, "tree_attention_workspace")
+        ws, wsb = _workspace(nbytes, dev, workspace)
+        code = lib().tree_attention(ctypes.byref(desc), batch, n, hq,
+                                    d ** -0.5 if scale is None else scale, _p(q),
+                                    (ctypes.c_int64 * 3)(*st), _p(k_cache), _p(v_cache),
+                                    _p(block_table), _p(ctx_len), _p(count), _p(mask), _p(out.out),
+                                    _p(out.lse), _p(out.status), _p(ws), wsb, s)
+    _raise(code, "tree_attention")
+    return out
+
+
+def kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+              ctx_len: torch.Tensor, count: torch.Tensor, accept_len: torch.Tensor,
+              accept_path: torch.Tensor, new_len: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None, stream=None):
+    """(new_len [batch] int64, status): the accepted nodes' K and V (accept_len [batch],
+    accept_path [batch][max_depth] int32, as tree_verify_accept writes them) move behind the
+    root in every layer of the caches [layers][n_pages][page_size][heads][head_dim] (or one
+    layer without that axis), in place; new_len = ctx_len + 1 + accept_len."""
+    s, ctx = _on(k_cache, "k_cache", stream)
+    dev = k_cache.device
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [batch][max_pages]")
+    batch, max_pages = block_table.shape
+    _check(block_table, "block_table", dev, dtype=torch.int32)
+    layered = k_cache.dim() == 5
+    desc, layer_stride = _cache(k_cache, v_cache, max_pages, layered)
+    _check(ctx_len, "ctx_len", dev, (batch,), torch.int64)
+    _check(count, "count", dev, (batch,), torch.int32)
+    _check(accept_len, "accept_len", dev, (batch,), torch.int32)
+    if not isinstance(accept_path, torch.Tensor) or accept_path.dim() != 2:
+        raise ValueError("accept_path must be [batch][max_depth]")
+    _check(accept_path, "accept_path", dev, (batch, accept_path.shape[1]), torch.int32)
+    with ctx:
+        if new_len is None:
+            new_len = torch.empty(batch, dtype=torch.int64, device=dev)
+        else:
+            _check(new_len, "new_len", dev, (batch,), torch.int64)
+            if new_len.data_ptr() == ctx_len.data_ptr():
+                raise ValueError("new_len must not be ctx_len")
+        if status is None:
+            status = torch.empty(batch, dtype=torch.int32, device=dev)
+        else:
+            _check(status, "status", dev, (batch,), torch.int32)
+        code = lib().kv_commit(ctypes.byref(desc), batch, k_cache.shape[0] if layered else 1,
+                               layer_stride, accept_path.shape[1], _p(k_cache), _p(v_cache),
+                               _p(block_table), _p(ctx_len), _p(count), _p(accept_len),
+                               _p(accept_path), _p(new_len), _p(status), s)
+    _raise(code, "kv_commit")
+    return new_len, status
 
 
 def trace_enable(on: bool = True) -> bool:

@@ -1,0 +1,238 @@
+// How tree attention's work is cut up, shared by its kernels.
+//
+// An item is (request b, kv head h, row tile mt): up to BM rows (node, query
+// head of the group) against klen = ctx_len + (last node of the tile + 1)
+// tokens, in ceil(klen / BK) key tiles. The units (key tiles of all items in
+// order) are divided evenly over the grid, so lengths from one token to the
+// longest balance without the host knowing them: a block's share may begin and
+// end inside items. An item inside one share is written out directly; the
+// pieces of a split item go to the workspace as (unnormalised fp32 sums, row
+// maximum, row sum), at most two a block (slot 0: the share's first item, slot
+// 1: its last), and the join kernel adds them up in unit order, so results do
+// not depend on timing.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace pct {
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct AttnParams {
+  int batch, n, hq, hkv, g, d, page_size, n_pages, max_pages, words;
+  float scale_log2;             // scale * log2 e
+  long long qs_b, qs_n, qs_h, ks_page, ks_slot, ks_head;
+  const void *q, *k, *v;
+  const int32_t* table;
+  const int64_t* ctx_len;
+  const int32_t* count;
+  const uint32_t* mask;
+  void* out;
+  float* lse;
+  int32_t* status;
+  float* po;                    // [grid][2][BM][d] pieces' sums
+  float2* pml;                  // [grid][2][BM] pieces' (maximum in log2 units, sum)
+  int4* meta;                   // [grid] split item begun by the block: b (-1 none),
+                                // h, mt, slot | last block << 1
+};
+
+struct Req {
+  long long ctx;
+  int n, st;                    // n = 0 when st != 0
+};
+__device__ __forceinline__ Req attn_req(const AttnParams& p, int b) {
+  Req r;
+  r.ctx = p.ctx_len[b];
+  r.n = p.count ? p.count[b] : p.n;
+  r.st = 0;
+  if (r.n < 0 || r.n > p.n) r.st |= PCT_DEV_BAD_COUNT;
+  if (r.ctx < 0 || (r.st == 0 && r.ctx + r.n > (long long)p.max_pages * p.page_size))
+    r.st |= PCT_DEV_BAD_LENGTH;
+  if (r.st) { r.n = 0; r.ctx = 0; }
+  return r;
+}
+
+template <int BM, int BK>
+struct Sched {
+  // tokens that the rows of tile mt see at most
+  static __device__ __forceinline__ int klen(const AttnParams& p, const Req& r, int mt) {
+    const int last = min(r.n, ((mt + 1) * BM - 1) / p.g + 1);
+    return (int)r.ctx + last;
+  }
+  static __device__ __forceinline__ int row_tiles(const AttnParams& p, const Req& r) {
+    return (r.n * p.g + BM - 1) / BM;
+  }
+  static __device__ long long head_units(const AttnParams& p, const Req& r) {
+    const int nm = row_tiles(p, r);
+    long long s = 0;
+    for (int mt = 0; mt < nm; ++mt) s += (klen(p, r, mt) + BK - 1) / BK;
+    return s;
+  }
+};
+
+// A block's place in the schedule. cur_* is the item of the next unit.
+struct Share {
+  long long u0, u1;             // units of this block
+  long long total, per, extra;  // per (+ 1 for the first `extra` blocks) units a block
+  int b, h, mt, tile;
+};
+__device__ __forceinline__ int block_of(const Share& s, long long u) {
+  const long long cut = s.extra * (s.per + 1);
+  return (int)(u < cut ? u / (s.per + 1) : s.extra + (u - cut) / s.per);
+}
+
+// Fills *out (shared memory); all NT threads call it. At least min_units go to
+// a block, so that pieces are not smaller than what joining them costs.
+template <int BM, int BK, int NT>
+__device__ void sched_begin(const AttnParams& p, int min_units, Share* out, long long* sums) {
+  typedef Sched<BM, BK> S;
+  const int tid = threadIdx.x;
+  const int seg = (p.batch + NT - 1) / NT;
+  const int b0 = tid * seg, b1 = min(p.batch, b0 + seg);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Req r = attn_req(p, b);
+    mine += S::head_units(p, r) * p.hkv;
+  }
+  const int lane = tid & 31, w = tid >> 5;
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) sums[w] = inc;
+  __syncthreads();
+  long long base = 0, total = 0;
+#pragma unroll
+  for (int k = 0; k < NT / 32; ++k) {
+    if (k < w) base += sums[k];
+    total += sums[k];
+  }
+  const long long ex = base + inc - mine;
+  long long blocks = (total + min_units - 1) / min_units;
+  if (blocks > gridDim.x) blocks = gridDim.x;
+  if (blocks < 1) blocks = 1;
+  const long long per = total / blocks, extra = total - per * blocks;
+  const long long c = blockIdx.x;
+  const long long u0 = c < blocks ? c * per + (c < extra ? c : extra) : total;
+  const long long u1 = c < blocks ? u0 + per + (c < extra ? 1 : 0) : total;
+  if (tid == 0) {
+    out->u0 = u0; out->u1 = u1; out->total = total; out->per = per; out->extra = extra;
+    out->b = -1; out->h = out->mt = out->tile = 0;
+  }
+  __syncthreads();
+  if (u0 < u1 && u0 >= ex && u0 < ex + mine) {
+    long long at = ex;
+    for (int b = b0; b < b1; ++b) {
+      const Req r = attn_req(p, b);
+      const long long hu = S::head_units(p, r), all = hu * p.hkv;
+      if (u0 < at + all) {
+        long long rest = u0 - at;
+        const int h = (int)(rest / hu);
+        rest -= h * hu;
+        int mt = 0;
+        for (;; ++mt) {
+          const int t = (S::klen(p, r, mt) + BK - 1) / BK;
+          if (rest < t) break;
+          rest -= t;
+        }
+        out->b = b; out->h = h; out->mt = mt; out->tile = (int)rest;
+        break;
+      }
+      at += all;
+    }
+  }
+  __syncthreads();
+}
+
+// Rows at or past count (and all rows of a refused request) to 0 and -inf, and
+// the status word, for requests blockIdx.x, blockIdx.x + grid, ...
+template <typename T>
+__device__ void attn_tail(const AttnParams& p) {
+  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+    const Req r = attn_req(p, b);
+    const int32_t* row = p.table + (long long)b * p.max_pages;
+    int bad = 0;
+    if (r.n > 0) {
+      const int e = (int)((r.ctx + r.n - 1) / p.page_size);
+      for (int k = threadIdx.x; k <= e; k += blockDim.x)
+        bad |= row[k] < 0 || row[k] >= p.n_pages;
+    }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) p.status[b] = r.st | (bad ? PCT_DEV_BAD_PAGE : 0);
+    const long long r0 = ((long long)b * p.n + r.n) * p.hq, r1 = ((long long)b * p.n + p.n) * p.hq;
+    const int vec = p.d * (int)sizeof(T) / 16;
+    uint4* o = static_cast<uint4*>(p.out);
+    for (long long i = r0 * vec + threadIdx.x; i < r1 * vec; i += blockDim.x)
+      o[i] = make_uint4(0, 0, 0, 0);
+    if (p.lse)
+      for (long long i = r0 + threadIdx.x; i < r1; i += blockDim.x) p.lse[i] = neg_inf();
+  }
+}
+
+__device__ __forceinline__ void store_out(float* p, float4 v) {
+  *reinterpret_cast<float4*>(p) = v;
+}
+__device__ __forceinline__ void store_out(__nv_bfloat16* p, float4 v) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  uint2 w;
+  w.x = *reinterpret_cast<uint32_t*>(&a);
+  w.y = *reinterpret_cast<uint32_t*>(&b);
+  *reinterpret_cast<uint2*>(p) = w;
+}
+
+// Joins the pieces of the split item that block blockIdx.x of the attention
+// kernel began: one warp a row, its lanes over head_dim, pieces in unit order.
+template <typename T, int BM>
+__global__ void __launch_bounds__(128) attn_join_kernel(AttnParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x;
+  const int4 m = p.meta[c];
+  if (m.x < 0) return;
+  const int b = m.x, h = m.y, mt = m.z, slot = m.w & 1, last = m.w >> 1;
+  const Req r = attn_req(p, b);
+  const int rows = min(BM, r.n * p.g - mt * BM);
+  const int lane = threadIdx.x & 31;
+  for (int i = blockIdx.y * 4 + (threadIdx.x >> 5); i < rows; i += gridDim.y * 4) {
+    float mx = neg_inf();
+    for (int k = c + lane; k <= last; k += 32)
+      mx = fmaxf(mx, p.pml[((long long)k * 2 + (k == c ? slot : 0)) * BM + i].x);
+    mx = warp_max(mx);
+    const float ref = mx == neg_inf() ? 0.f : mx;
+    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    float l = 0.f;
+    for (int k = c; k <= last; ++k) {
+      const long long at = ((long long)k * 2 + (k == c ? slot : 0)) * BM + i;
+      const float2 ml = p.pml[at];
+      const float w = ex2(ml.x - ref);
+      l += ml.y * w;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int d0 = j * 128 + lane * 4;
+        if (d0 < p.d) {
+          const float4 x = *reinterpret_cast<const float4*>(p.po + at * p.d + d0);
+          acc[j].x = fmaf(x.x, w, acc[j].x); acc[j].y = fmaf(x.y, w, acc[j].y);
+          acc[j].z = fmaf(x.z, w, acc[j].z); acc[j].w = fmaf(x.w, w, acc[j].w);
+        }
+      }
+    }
+    const int row = mt * BM + i, node = row / p.g, qh = h * p.g + row % p.g;
+    const long long o = ((long long)b * p.n + node) * p.hq + qh;
+    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int d0 = j * 128 + lane * 4;
+      if (d0 < p.d)
+        store_out(static_cast<T*>(p.out) + o * p.d + d0,
+                  make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv));
+    }
+    if (p.lse && lane == 0) p.lse[o] = l > 0.f ? (ref + __log2f(l)) * kLn2 : (l == l ? neg_inf() : l);
+  }
+}
+
+}  // namespace
+}  // namespace pct

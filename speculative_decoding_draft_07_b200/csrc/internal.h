@@ -208,6 +208,44 @@ struct FinalArgs {
 };
 cudaError_t launch_final(const FinalArgs& a, cudaStream_t s);
 
+// ---- paged key-value cache (kv_cache.cu) --------------------------------------
+cudaError_t launch_kv_pages_resize(int batch, int page_size, int max_pages, int n_pages,
+                                   const int64_t* ctx_len, const int32_t* count,
+                                   int32_t* block_table, int32_t* held, int32_t* free_pages,
+                                   int32_t* free_count, int32_t* status, cudaStream_t s);
+cudaError_t launch_kv_tree_slots(int batch, int n_stride, int page_size, int max_pages,
+                                 int n_pages, const int64_t* ctx_len, const int32_t* count,
+                                 const int32_t* depth, const int32_t* block_table, int64_t* slot,
+                                 int64_t* pos, int32_t* status, cudaStream_t s);
+cudaError_t launch_kv_append(const kv_cache_desc& d, int batch, int n_stride, const void* k_new,
+                             const void* v_new, const int64_t* new_stride, const int64_t* slot,
+                             void* k_cache, void* v_cache, int32_t* status, cudaStream_t s);
+cudaError_t launch_kv_commit(const kv_cache_desc& d, int batch, int layers, int64_t layer_stride,
+                             int max_depth, void* k_cache, void* v_cache,
+                             const int32_t* block_table, const int64_t* ctx_len,
+                             const int32_t* count, const int32_t* accept_len,
+                             const int32_t* accept_path, int64_t* new_len, int32_t* status,
+                             cudaStream_t s);
+
+// ---- tree attention (tree_attn*.cu) -------------------------------------------
+struct AttnArgs {
+  kv_cache_desc kv;
+  int batch, n, hq;             // n = n_stride
+  float scale;
+  const void* q;
+  int64_t qs_b, qs_n, qs_h;
+  const void *k, *v;
+  const int32_t* table;
+  const int64_t* ctx_len;
+  const int32_t* count;         // or null
+  const uint32_t* mask;         // or null
+  void* out;
+  float* lse;                   // or null
+  int32_t* status;
+};
+size_t attn_workspace(const kv_cache_desc& kv, int batch, int n, int hq);
+cudaError_t launch_attn(const AttnArgs& a, void* ws, cudaStream_t s);
+
 // pct_score_parents: per-row merge of partials into lse + top-k.
 cudaError_t launch_rows_finalize(int rows, int k, int S, Partials part, float* lse,
                                  int32_t* top_tok, float* top_logpi, const int32_t* err,

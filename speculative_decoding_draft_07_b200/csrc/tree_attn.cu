@@ -1,0 +1,286 @@
+// Tree attention on the FP32 pipes: the host side that picks a kernel, and the
+// kernel for fp32 caches.
+//
+// One pass over the keys with the running maximum and sum of the softmax. A
+// block of 128 threads holds BM = 8 * RPT rows of Q in shared memory and steps
+// through key tiles of BK = 32 tokens: scores as 8 x 16 thread cells of RPT x 2,
+// the softmax by the 16 threads of a row group, and the weighted sum of V as
+// cells of RPT rows x head_dim / 16 columns in registers.
+#include "attn_sched.cuh"
+
+namespace pct {
+namespace {
+
+constexpr int kSimtThreads = 128;
+constexpr int kSimtBK = 32;
+
+template <typename T> __device__ __forceinline__ float4 load4(const T* p);
+template <> __device__ __forceinline__ float4 load4<float>(const float* p) {
+  return __ldg(reinterpret_cast<const float4*>(p));
+}
+template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+}
+
+// DC: columns of head_dim a thread accumulates (head_dim <= 16 * DC).
+template <typename T, int RPT, int DC>
+__global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(AttnParams p) {
+  constexpr int BM = 8 * RPT, BK = kSimtBK, NT = kSimtThreads;
+  typedef Sched<BM, BK> S;
+  extern __shared__ __align__(16) float sm[];
+  __shared__ Share share;
+  __shared__ long long sums[NT / 32];
+  __shared__ uint32_t seen[BM];            // visible keys of the tile, one bit a key
+  const int dp = p.d + 4;                  // row stride: 16-byte phases of 8 rows differ
+  float* Qs = sm;                          // [BM][dp]
+  float* Ks = Qs + BM * dp;                // [BK][dp]
+  float* Vs = Ks + BK * dp;                // [BK][dp]
+  float* Ps = Vs + BK * dp;                // [BK][BM]
+  const int tid = threadIdx.x, rg = tid >> 4, cg = tid & 15;
+  sched_begin<BM, BK, NT>(p, 2, &share, sums);
+  int4 begun = make_int4(-1, 0, 0, 0);
+
+  long long u = share.u0;
+  int b = share.b, h = share.h, mt = share.mt, t0 = share.tile;
+  while (u < share.u1) {
+    Req r = attn_req(p, b);
+    const int nm = S::row_tiles(p, r);
+    if (mt >= nm) { mt = 0; ++h; }
+    while (h >= p.hkv || r.n == 0) { ++b; h = 0; mt = 0; r = attn_req(p, b); }
+    const int klen = S::klen(p, r, mt), nt = (klen + BK - 1) / BK;
+    const int t1 = (int)min((long long)nt, t0 + (share.u1 - u));
+    const int row0 = mt * BM, rows = min(BM, r.n * p.g - row0);
+    const int32_t* table = p.table + (long long)b * p.max_pages;
+
+    __syncthreads();
+    const int v4 = p.d / 4;
+    for (int i = tid; i < BM * v4; i += NT) {
+      const int rr = i / v4, c = (i - rr * v4) * 4;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (rr < rows) {
+        const int row = row0 + rr, node = row / p.g, qh = h * p.g + (row - node * p.g);
+        x = load4(static_cast<const T*>(p.q) + b * p.qs_b + node * p.qs_n + qh * p.qs_h + c);
+      }
+      *reinterpret_cast<float4*>(Qs + rr * dp + c) = x;
+    }
+    float m[RPT], l[RPT], acc[RPT][DC];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      m[i] = neg_inf();
+      l[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < DC; ++j) acc[i][j] = 0.f;
+    }
+    for (int t = t0; t < t1; ++t) {
+      const int k0 = t * BK;
+      __syncthreads();
+      for (int i = tid; i < BK * v4; i += NT) {
+        const int kk = i / v4, c = (i - kk * v4) * 4, tok = k0 + kk;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (tok < klen) {
+          const int col = tok / p.page_size, page = table[col];
+          if (page >= 0 && page < p.n_pages) {
+            const long long at =
+                page * p.ks_page + (tok - col * p.page_size) * p.ks_slot + h * p.ks_head + c;
+            x = load4(static_cast<const T*>(p.k) + at);
+            y = load4(static_cast<const T*>(p.v) + at);
+          }
+        }
+        *reinterpret_cast<float4*>(Ks + kk * dp + c) = x;
+        *reinterpret_cast<float4*>(Vs + kk * dp + c) = y;
+      }
+      if (tid < BM) {
+        uint32_t bits = 0;
+        if (tid < rows) {
+          const int node = (row0 + tid) / p.g;
+          for (int kk = 0; kk < BK; ++kk) {
+            const int tok = k0 + kk, j = tok - (int)r.ctx;
+            bool on = tok < klen && j <= node;
+            if (on && j >= 0 && p.mask)
+              on = (p.mask[((long long)b * p.n + node) * p.words + (j >> 5)] >> (j & 31)) & 1u;
+            if (on) {
+              const int page = table[tok / p.page_size];
+              on = page >= 0 && page < p.n_pages;
+            }
+            bits |= (on ? 1u : 0u) << kk;
+          }
+        }
+        seen[tid] = bits;
+      }
+      __syncthreads();
+      float s[RPT][2];
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) s[i][0] = s[i][1] = 0.f;
+      for (int c = 0; c < p.d; c += 4) {
+        const float4 ka = *reinterpret_cast<const float4*>(Ks + cg * dp + c);
+        const float4 kb = *reinterpret_cast<const float4*>(Ks + (cg + 16) * dp + c);
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) {
+          const float4 x = *reinterpret_cast<const float4*>(Qs + (rg * RPT + i) * dp + c);
+          s[i][0] = fmaf(x.x, ka.x, fmaf(x.y, ka.y, fmaf(x.z, ka.z, fmaf(x.w, ka.w, s[i][0]))));
+          s[i][1] = fmaf(x.x, kb.x, fmaf(x.y, kb.y, fmaf(x.z, kb.z, fmaf(x.w, kb.w, s[i][1]))));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        const uint32_t bits = seen[rg * RPT + i];
+        s[i][0] = (bits >> cg) & 1u ? s[i][0] * p.scale_log2 : neg_inf();
+        s[i][1] = (bits >> (cg + 16)) & 1u ? s[i][1] * p.scale_log2 : neg_inf();
+        float mx = fmaxf(s[i][0], s[i][1]);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float mn = fmaxf(m[i], mx);
+        const float ref = mn == neg_inf() ? 0.f : mn;
+        const float f = ex2(m[i] - ref);
+        const float e0 = ex2(s[i][0] - ref), e1 = ex2(s[i][1] - ref);
+        float sum = e0 + e1;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l[i] = l[i] * f + sum;
+        m[i] = mn;
+#pragma unroll
+        for (int j = 0; j < DC; ++j) acc[i][j] *= f;
+        Ps[cg * BM + rg * RPT + i] = e0;
+        Ps[(cg + 16) * BM + rg * RPT + i] = e1;
+      }
+      __syncthreads();
+#pragma unroll 4
+      for (int kk = 0; kk < BK; ++kk) {
+        float pr[RPT];
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) pr[i] = Ps[kk * BM + rg * RPT + i];
+#pragma unroll
+        for (int q = 0; q < DC / 4; ++q) {
+          const int c = q * 64 + cg * 4;
+          if (c < p.d) {
+            const float4 v = *reinterpret_cast<const float4*>(Vs + kk * dp + c);
+#pragma unroll
+            for (int i = 0; i < RPT; ++i) {
+              acc[i][q * 4 + 0] = fmaf(pr[i], v.x, acc[i][q * 4 + 0]);
+              acc[i][q * 4 + 1] = fmaf(pr[i], v.y, acc[i][q * 4 + 1]);
+              acc[i][q * 4 + 2] = fmaf(pr[i], v.z, acc[i][q * 4 + 2]);
+              acc[i][q * 4 + 3] = fmaf(pr[i], v.w, acc[i][q * 4 + 3]);
+            }
+          }
+        }
+      }
+    }
+    const bool whole = t0 == 0 && t1 == nt;
+    const int slot = u == share.u0 ? 0 : 1;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const int rr = rg * RPT + i;
+      if (rr >= rows) continue;
+      if (whole) {
+        const int row = row0 + rr, node = row / p.g, qh = h * p.g + (row - node * p.g);
+        const long long o = ((long long)b * p.n + node) * p.hq + qh;
+        const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == l[i] ? 0.f : l[i]);
+#pragma unroll
+        for (int q = 0; q < DC / 4; ++q) {
+          const int c = q * 64 + cg * 4;
+          if (c < p.d)
+            store_out(static_cast<T*>(p.out) + o * p.d + c,
+                      make_float4(acc[i][q * 4] * inv, acc[i][q * 4 + 1] * inv,
+                                  acc[i][q * 4 + 2] * inv, acc[i][q * 4 + 3] * inv));
+        }
+        if (p.lse && cg == 0)
+          p.lse[o] = l[i] > 0.f ? (m[i] + __log2f(l[i])) * kLn2 : (l[i] == l[i] ? neg_inf() : l[i]);
+      } else {
+        const long long at = ((long long)blockIdx.x * 2 + slot) * BM + rr;
+#pragma unroll
+        for (int q = 0; q < DC / 4; ++q) {
+          const int c = q * 64 + cg * 4;
+          if (c < p.d)
+            *reinterpret_cast<float4*>(p.po + at * p.d + c) = make_float4(
+                acc[i][q * 4], acc[i][q * 4 + 1], acc[i][q * 4 + 2], acc[i][q * 4 + 3]);
+        }
+        if (cg == 0) p.pml[at] = make_float2(m[i], l[i]);
+      }
+    }
+    if (t0 == 0 && t1 < nt)
+      begun = make_int4(b, h, mt, slot | block_of(share, u + nt - 1) << 1);
+    u += t1 - t0;
+    t0 = 0;
+    ++mt;
+  }
+  if (tid == 0) p.meta[blockIdx.x] = begun;
+  attn_tail<T>(p);
+}
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
+
+struct AttnPlan {
+  int rpt, bm, grid;
+  size_t o_po, o_ml, o_meta, total;
+};
+AttnPlan plan(const kv_cache_desc& kv, int batch, int n, int hq) {
+  AttnPlan P;
+  const int g = hq / kv.heads_kv;
+  const long long rows = (long long)n * g;
+  P.rpt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  P.bm = 8 * P.rpt;
+  P.grid = num_sms() * 2;
+  size_t o = 0;
+  P.o_po = o;   o += align_up((size_t)P.grid * 2 * P.bm * kv.head_dim * sizeof(float));
+  P.o_ml = o;   o += align_up((size_t)P.grid * 2 * P.bm * sizeof(float2));
+  P.o_meta = o; o += align_up((size_t)P.grid * sizeof(int4));
+  P.total = o;
+  return P;
+}
+
+template <typename T, int RPT, int DC>
+cudaError_t run_simt(const AttnParams& p, const AttnPlan& P, cudaStream_t s) {
+  constexpr int BM = 8 * RPT;
+  const size_t smem = ((size_t)(BM + 2 * kSimtBK) * (p.d + 4) + kSimtBK * BM) * sizeof(float);
+  cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<T, RPT, DC>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  {
+    TraceScope t(s, "attn_simt");
+    attn_simt_kernel<T, RPT, DC><<<P.grid, kSimtThreads, smem, s>>>(p);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return e;
+  TraceScope t(s, "attn_join");
+  return launch_pdl(attn_join_kernel<T, BM>, dim3(P.grid, (BM + 7) / 8), dim3(128), 0, s, 1, p);
+}
+template <typename T, int RPT>
+cudaError_t run_simt_d(const AttnParams& p, const AttnPlan& P, cudaStream_t s) {
+  if (p.d <= 64) return run_simt<T, RPT, 4>(p, P, s);
+  if (p.d <= 128) return run_simt<T, RPT, 8>(p, P, s);
+  return run_simt<T, RPT, 16>(p, P, s);
+}
+template <typename T>
+cudaError_t run_simt_r(const AttnParams& p, const AttnPlan& P, cudaStream_t s) {
+  if (P.rpt == 1) return run_simt_d<T, 1>(p, P, s);
+  if (P.rpt == 2) return run_simt_d<T, 2>(p, P, s);
+  return run_simt_d<T, 4>(p, P, s);
+}
+
+}  // namespace
+
+size_t attn_workspace(const kv_cache_desc& kv, int batch, int n, int hq) {
+  return plan(kv, batch, n, hq).total;
+}
+
+cudaError_t launch_attn(const AttnArgs& a, void* ws, cudaStream_t s) {
+  const AttnPlan P = plan(a.kv, a.batch, a.n, a.hq);
+  char* w = static_cast<char*>(ws);
+  AttnParams p;
+  p.batch = a.batch; p.n = a.n; p.hq = a.hq; p.hkv = a.kv.heads_kv; p.g = a.hq / a.kv.heads_kv;
+  p.d = a.kv.head_dim; p.page_size = a.kv.page_size; p.n_pages = a.kv.n_pages;
+  p.max_pages = a.kv.max_pages; p.words = (a.n + 31) / 32;
+  p.scale_log2 = a.scale * kLog2e;
+  p.qs_b = a.qs_b; p.qs_n = a.qs_n; p.qs_h = a.qs_h;
+  p.ks_page = a.kv.page_stride; p.ks_slot = a.kv.slot_stride; p.ks_head = a.kv.head_stride;
+  p.q = a.q; p.k = a.k; p.v = a.v; p.table = a.table; p.ctx_len = a.ctx_len; p.count = a.count;
+  p.mask = a.mask; p.out = a.out; p.lse = a.lse; p.status = a.status;
+  p.po = reinterpret_cast<float*>(w + P.o_po);
+  p.pml = reinterpret_cast<float2*>(w + P.o_ml);
+  p.meta = reinterpret_cast<int4*>(w + P.o_meta);
+  return a.kv.dtype == PCT_BF16 ? run_simt_r<__nv_bfloat16>(p, P, s) : run_simt_r<float>(p, P, s);
+}
+
+}  // namespace pct
