@@ -16,9 +16,6 @@
 #include "internal.h"
 
 namespace pct {
-namespace {
-
-constexpr float kLn2 = 0.6931471805599453f;
 
 struct AttnParams {
   int batch, n, hq, hkv, g, d, page_size, n_pages, max_pages, words;
@@ -34,9 +31,14 @@ struct AttnParams {
   int32_t* status;
   float* po;                    // [grid][2][BM][d] pieces' sums
   float2* pml;                  // [grid][2][BM] pieces' (maximum in log2 units, sum)
+  uint32_t pg_mul, pg_shift;    // t / page_size = (umulhi(t, mul) + t) >> shift
   int4* meta;                   // [grid] split item begun by the block: b (-1 none),
                                 // h, mt, slot | last block << 1
 };
+
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct Req {
   long long ctx;
@@ -52,6 +54,28 @@ __device__ __forceinline__ Req attn_req(const AttnParams& p, int b) {
     r.st |= PCT_DEV_BAD_LENGTH;
   if (r.st) { r.n = 0; r.ctx = 0; }
   return r;
+}
+
+// t / page_size for 0 <= t < 2^31 without a division (round-up reciprocal of 32
+// + shift bits, Granlund and Montgomery 1994)
+__device__ __forceinline__ uint32_t page_of(const AttnParams& p, uint32_t t) {
+  return (__umulhi(t, p.pg_mul) + t) >> p.pg_shift;
+}
+
+// Which of the 32 tokens at node offsets j .. j + 31 (negative: context) row
+// `node` sees; `words` is its mask row or null for a causal chain.
+__device__ __forceinline__ uint32_t seen32(const AttnParams& p, const uint32_t* words, int node,
+                                           int j) {
+  const int live = node - j + 1;
+  if (live <= 0) return 0u;
+  uint32_t bits = 0xffffffffu;
+  if (words && j > -32) {
+    const int w = j >> 5, sh = j & 31;
+    const uint32_t lo = w < 0 ? 0xffffffffu : w < p.words ? __ldg(words + w) : 0u;
+    const uint32_t hi = w + 1 < p.words ? __ldg(words + w + 1) : 0u;
+    bits = __funnelshift_r(lo, hi, sh);
+  }
+  return live < 32 ? bits & ((1u << live) - 1u) : bits;
 }
 
 template <int BM, int BK>

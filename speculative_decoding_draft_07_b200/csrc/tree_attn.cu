@@ -1,30 +1,33 @@
-// Tree attention on the FP32 pipes: the host side that picks a kernel, and the
-// kernel for fp32 caches.
+// Tree attention: the host side that picks a kernel, and the kernel for fp32
+// caches, on the FP32 pipes.
 //
 // One pass over the keys with the running maximum and sum of the softmax. A
 // block of 128 threads holds BM = 8 * RPT rows of Q in shared memory and steps
 // through key tiles of BK = 32 tokens: scores as 8 x 16 thread cells of RPT x 2,
 // the softmax by the 16 threads of a row group, and the weighted sum of V as
 // cells of RPT rows x head_dim / 16 columns in registers.
+#include <algorithm>
+
 #include "attn_sched.cuh"
 
 namespace pct {
+
+// attn_mma.cu
+int attn_mma_rows(int rows);
+int attn_mma_blocks(int d);
+cudaError_t launch_attn_mma(const AttnParams& p, int bm, int grid, cudaStream_t s);
+
 namespace {
 
 constexpr int kSimtThreads = 128;
 constexpr int kSimtBK = 32;
 
-template <typename T> __device__ __forceinline__ float4 load4(const T* p);
-template <> __device__ __forceinline__ float4 load4<float>(const float* p) {
+__device__ __forceinline__ float4 load4(const float* p) {
   return __ldg(reinterpret_cast<const float4*>(p));
-}
-template <> __device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-  return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
 }
 
 // DC: columns of head_dim a thread accumulates (head_dim <= 16 * DC).
-template <typename T, int RPT, int DC>
+template <int RPT, int DC>
 __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(AttnParams p) {
   constexpr int BM = 8 * RPT, BK = kSimtBK, NT = kSimtThreads;
   typedef Sched<BM, BK> S;
@@ -60,7 +63,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(AttnParams p) {
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (rr < rows) {
         const int row = row0 + rr, node = row / p.g, qh = h * p.g + (row - node * p.g);
-        x = load4(static_cast<const T*>(p.q) + b * p.qs_b + node * p.qs_n + qh * p.qs_h + c);
+        x = load4(static_cast<const float*>(p.q) + b * p.qs_b + node * p.qs_n + qh * p.qs_h + c);
       }
       *reinterpret_cast<float4*>(Qs + rr * dp + c) = x;
     }
@@ -83,8 +86,8 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(AttnParams p) {
           if (page >= 0 && page < p.n_pages) {
             const long long at =
                 page * p.ks_page + (tok - col * p.page_size) * p.ks_slot + h * p.ks_head + c;
-            x = load4(static_cast<const T*>(p.k) + at);
-            y = load4(static_cast<const T*>(p.v) + at);
+            x = load4(static_cast<const float*>(p.k) + at);
+            y = load4(static_cast<const float*>(p.v) + at);
           }
         }
         *reinterpret_cast<float4*>(Ks + kk * dp + c) = x;
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(AttnParams p) {
         for (int q = 0; q < DC / 4; ++q) {
           const int c = q * 64 + cg * 4;
           if (c < p.d)
-            store_out(static_cast<T*>(p.out) + o * p.d + c,
+            store_out(static_cast<float*>(p.out) + o * p.d + c,
                       make_float4(acc[i][q * 4] * inv, acc[i][q * 4 + 1] * inv,
                                   acc[i][q * 4 + 2] * inv, acc[i][q * 4 + 3] * inv));
         }
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(AttnParams p) {
     ++mt;
   }
   if (tid == 0) p.meta[blockIdx.x] = begun;
-  attn_tail<T>(p);
+  attn_tail<float>(p);
 }
 
 constexpr size_t kAlign = 256;
@@ -219,9 +222,15 @@ AttnPlan plan(const kv_cache_desc& kv, int batch, int n, int hq) {
   AttnPlan P;
   const int g = hq / kv.heads_kv;
   const long long rows = (long long)n * g;
-  P.rpt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-  P.bm = 8 * P.rpt;
-  P.grid = num_sms() * 2;
+  if (kv.dtype == PCT_BF16) {
+    P.rpt = 0;
+    P.bm = attn_mma_rows((int)std::min<long long>(rows, 1 << 20));
+    P.grid = num_sms() * attn_mma_blocks(kv.head_dim);
+  } else {
+    P.rpt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    P.bm = 8 * P.rpt;
+    P.grid = num_sms() * 2;
+  }
   size_t o = 0;
   P.o_po = o;   o += align_up((size_t)P.grid * 2 * P.bm * kv.head_dim * sizeof(float));
   P.o_ml = o;   o += align_up((size_t)P.grid * 2 * P.bm * sizeof(float2));
@@ -230,33 +239,32 @@ AttnPlan plan(const kv_cache_desc& kv, int batch, int n, int hq) {
   return P;
 }
 
-template <typename T, int RPT, int DC>
+template <int RPT, int DC>
 cudaError_t run_simt(const AttnParams& p, const AttnPlan& P, cudaStream_t s) {
   constexpr int BM = 8 * RPT;
   const size_t smem = ((size_t)(BM + 2 * kSimtBK) * (p.d + 4) + kSimtBK * BM) * sizeof(float);
-  cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<T, RPT, DC>,
+  cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<RPT, DC>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   {
     TraceScope t(s, "attn_simt");
-    attn_simt_kernel<T, RPT, DC><<<P.grid, kSimtThreads, smem, s>>>(p);
+    attn_simt_kernel<RPT, DC><<<P.grid, kSimtThreads, smem, s>>>(p);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
   TraceScope t(s, "attn_join");
-  return launch_pdl(attn_join_kernel<T, BM>, dim3(P.grid, (BM + 7) / 8), dim3(128), 0, s, 1, p);
+  return launch_pdl(attn_join_kernel<float, BM>, dim3(P.grid, (BM + 7) / 8), dim3(128), 0, s, 1, p);
 }
-template <typename T, int RPT>
+template <int RPT>
 cudaError_t run_simt_d(const AttnParams& p, const AttnPlan& P, cudaStream_t s) {
-  if (p.d <= 64) return run_simt<T, RPT, 4>(p, P, s);
-  if (p.d <= 128) return run_simt<T, RPT, 8>(p, P, s);
-  return run_simt<T, RPT, 16>(p, P, s);
+  if (p.d <= 64) return run_simt<RPT, 4>(p, P, s);
+  if (p.d <= 128) return run_simt<RPT, 8>(p, P, s);
+  return run_simt<RPT, 16>(p, P, s);
 }
-template <typename T>
 cudaError_t run_simt_r(const AttnParams& p, const AttnPlan& P, cudaStream_t s) {
-  if (P.rpt == 1) return run_simt_d<T, 1>(p, P, s);
-  if (P.rpt == 2) return run_simt_d<T, 2>(p, P, s);
-  return run_simt_d<T, 4>(p, P, s);
+  if (P.rpt == 1) return run_simt_d<1>(p, P, s);
+  if (P.rpt == 2) return run_simt_d<2>(p, P, s);
+  return run_simt_d<4>(p, P, s);
 }
 
 }  // namespace
@@ -275,12 +283,15 @@ cudaError_t launch_attn(const AttnArgs& a, void* ws, cudaStream_t s) {
   p.scale_log2 = a.scale * kLog2e;
   p.qs_b = a.qs_b; p.qs_n = a.qs_n; p.qs_h = a.qs_h;
   p.ks_page = a.kv.page_stride; p.ks_slot = a.kv.slot_stride; p.ks_head = a.kv.head_stride;
+  p.pg_shift = 0;
+  while ((1u << p.pg_shift) < (unsigned)p.page_size) ++p.pg_shift;
+  p.pg_mul = (uint32_t)(((1ull << 32) * ((1ull << p.pg_shift) - p.page_size)) / p.page_size + 1);
   p.q = a.q; p.k = a.k; p.v = a.v; p.table = a.table; p.ctx_len = a.ctx_len; p.count = a.count;
   p.mask = a.mask; p.out = a.out; p.lse = a.lse; p.status = a.status;
   p.po = reinterpret_cast<float*>(w + P.o_po);
   p.pml = reinterpret_cast<float2*>(w + P.o_ml);
   p.meta = reinterpret_cast<int4*>(w + P.o_meta);
-  return a.kv.dtype == PCT_BF16 ? run_simt_r<__nv_bfloat16>(p, P, s) : run_simt_r<float>(p, P, s);
+  return a.kv.dtype == PCT_BF16 ? launch_attn_mma(p, P.bm, P.grid, s) : run_simt_r(p, P, s);
 }
 
 }  // namespace pct
