@@ -31,6 +31,8 @@ struct AttnParams {
   int32_t* status;
   float* po;                    // [grid][2][BM][d] pieces' sums
   float2* pml;                  // [grid][2][BM] pieces' (maximum in log2 units, sum)
+  int32_t* fail;                // [grid] set by a block whose bounded wait gave up, or null
+  uint32_t q_sign;              // flips the signs of a pair of bf16 queries (scale < 0)
   uint32_t pg_mul, pg_shift;    // t / page_size = (umulhi(t, mul) + t) >> shift
   int4* meta;                   // [grid] split item begun by the block: b (-1 none),
                                 // h, mt, slot | last block << 1
@@ -215,6 +217,8 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnParams p) {
   pdl_wait();
   pdl_trigger();
   const int c = blockIdx.x;
+  if (p.fail && blockIdx.y == 0 && p.fail[c])
+    for (int b = threadIdx.x; b < p.batch; b += blockDim.x) atomicOr(p.status + b, PCT_DEV_TIMEOUT);
   const int4 m = p.meta[c];
   if (m.x < 0) return;
   const int b = m.x, h = m.y, mt = m.z, slot = m.w & 1, last = m.w >> 1;

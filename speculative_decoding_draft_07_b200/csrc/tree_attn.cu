@@ -16,6 +16,10 @@ namespace pct {
 int attn_mma_rows(int rows);
 int attn_mma_blocks(int d);
 cudaError_t launch_attn_mma(const AttnParams& p, int bm, int grid, cudaStream_t s);
+// attn_umma.cu
+int attn_umma_rows();
+bool attn_umma_pages(int page_size);
+cudaError_t launch_attn_umma(const AttnParams& p, int grid, cudaStream_t s);
 
 namespace {
 
@@ -215,13 +219,15 @@ constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
 
 struct AttnPlan {
-  int rpt, bm, grid;
-  size_t o_po, o_ml, o_meta, total;
+  bool umma;                    // try the tcgen05 kernel first
+  int rpt, bm, grid;            // of the other kernels
+  size_t o_po, o_ml, o_meta, o_fail, total;
 };
 AttnPlan plan(const kv_cache_desc& kv, int batch, int n, int hq) {
   AttnPlan P;
   const int g = hq / kv.heads_kv;
   const long long rows = (long long)n * g;
+  P.umma = kv.dtype == PCT_BF16 && rows > 64 && kv.head_dim <= 128 && attn_umma_pages(kv.page_size);
   if (kv.dtype == PCT_BF16) {
     P.rpt = 0;
     P.bm = attn_mma_rows((int)std::min<long long>(rows, 1 << 20));
@@ -231,10 +237,13 @@ AttnPlan plan(const kv_cache_desc& kv, int batch, int n, int hq) {
     P.bm = 8 * P.rpt;
     P.grid = num_sms() * 2;
   }
+  size_t prows = (size_t)P.grid * 2 * P.bm;
+  if (P.umma) prows = std::max(prows, (size_t)num_sms() * 2 * attn_umma_rows());
   size_t o = 0;
-  P.o_po = o;   o += align_up((size_t)P.grid * 2 * P.bm * kv.head_dim * sizeof(float));
-  P.o_ml = o;   o += align_up((size_t)P.grid * 2 * P.bm * sizeof(float2));
+  P.o_po = o;   o += align_up(prows * kv.head_dim * sizeof(float));
+  P.o_ml = o;   o += align_up(prows * sizeof(float2));
   P.o_meta = o; o += align_up((size_t)P.grid * sizeof(int4));
+  P.o_fail = o; o += align_up((size_t)P.grid * sizeof(int32_t));
   P.total = o;
   return P;
 }
@@ -291,6 +300,16 @@ cudaError_t launch_attn(const AttnArgs& a, void* ws, cudaStream_t s) {
   p.po = reinterpret_cast<float*>(w + P.o_po);
   p.pml = reinterpret_cast<float2*>(w + P.o_ml);
   p.meta = reinterpret_cast<int4*>(w + P.o_meta);
+  p.fail = nullptr;
+  p.q_sign = 0;
+  // scale 0 stays off the tcgen05 kernel, which scales masked (-inf) scores
+  if (P.umma && a.scale != 0.f) {
+    AttnParams up = p;
+    up.fail = reinterpret_cast<int32_t*>(w + P.o_fail);
+    if (a.scale < 0.f) { up.scale_log2 = -p.scale_log2; up.q_sign = 0x80008000u; }
+    const cudaError_t e = launch_attn_umma(up, num_sms(), s);
+    if (e != cudaErrorNotSupported) return e;   // strides a tensor map cannot hold: the other kernel
+  }
   return a.kv.dtype == PCT_BF16 ? launch_attn_mma(p, P.bm, P.grid, s) : run_simt_r(p, P, s);
 }
 
