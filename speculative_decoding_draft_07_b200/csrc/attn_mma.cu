@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<DP>::MINB) attn_mma_kern
   constexpr int CH = DP / 8;                           // 16-byte pieces a row
   constexpr int STAGES = MmaShape<DP>::STAGES, TILE = MmaShape<DP>::TILE;
   constexpr bool QREG = DP <= 128;                     // Q fragments stay in registers
-  typedef Sched<BM, BK> S;
+  typedef Sched<BK> S;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Share share;
   __shared__ long long sums[NT / 32];
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<DP>::MINB) attn_mma_kern
   float* obuf = reinterpret_cast<float*>(ring);        // [WK][BM][DP + 8] at an item's end
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wm = warp % WM, wk = warp / WM;
   if (tid < STAGES) gone[tid] = 0;
-  sched_begin<BM, BK, NT>(p, 1, &share, sums);
+  sched_begin<BK, NT>(p, 1, &share, sums);
   int4 begun = make_int4(-1, 0, 0, 0);
 
   long long u = share.u0;
@@ -308,10 +308,10 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<DP>::MINB) attn_mma_kern
       if (whole) {
         const int row = row0 + rr, nd = row / p.g, qh = h * p.g + (row - nd * p.g);
         const long long o = ((long long)b * p.n + nd) * p.hq + qh;
-        const float inv = sum > 0.f ? 1.f / sum : (sum == sum ? 0.f : sum);
+        const float inv = inverse(sum);
         store_out(static_cast<__nv_bfloat16*>(p.out) + o * p.d + c,
                   make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
-        if (p.lse && c == 0) p.lse[o] = sum > 0.f ? (ref + __log2f(sum)) * kLn2 : (sum == sum ? neg_inf() : sum);
+        if (p.lse && c == 0) p.lse[o] = lse_of(ref, sum);
       } else {
         const long long at = ((long long)blockIdx.x * 2 + slot) * BM + rr;
         *reinterpret_cast<float4*>(p.po + at * p.d + c) = x;

@@ -1,6 +1,6 @@
 // How tree attention's work is cut up, shared by its kernels.
 //
-// An item is (request b, kv head h, row tile mt): up to BM rows (node, query
+// An item is (request b, kv head h, row tile mt): up to bm rows (node, query
 // head of the group) against klen = ctx_len + (last node of the tile + 1)
 // tokens, in ceil(klen / BK) key tiles. The units (key tiles of all items in
 // order) are divided evenly over the grid, so lengths from one token to the
@@ -29,10 +29,10 @@ struct AttnParams {
   void* out;
   float* lse;
   int32_t* status;
-  float* po;                    // [grid][2][BM][d] pieces' sums
-  float2* pml;                  // [grid][2][BM] pieces' (maximum in log2 units, sum)
-  int32_t* fail;                // [grid] set by a block whose bounded wait gave up, or null
-  uint32_t q_sign;              // flips the signs of a pair of bf16 queries (scale < 0)
+  float* po;                    // [grid][2][bm][d] pieces' sums
+  float2* pml;                  // [grid][2][bm] pieces' (maximum in log2 units, sum)
+  int32_t* fail;                // [grid] set by a block whose bounded wait gave up (attn_umma)
+  int bm;                       // rows of an item
   uint32_t pg_mul, pg_shift;    // t / page_size = (umulhi(t, mul) + t) >> shift
   int4* meta;                   // [grid] split item begun by the block: b (-1 none),
                                 // h, mt, slot | last block << 1
@@ -80,15 +80,15 @@ __device__ __forceinline__ uint32_t seen32(const AttnParams& p, const uint32_t* 
   return live < 32 ? bits & ((1u << live) - 1u) : bits;
 }
 
-template <int BM, int BK>
+template <int BK>
 struct Sched {
   // tokens that the rows of tile mt see at most
   static __device__ __forceinline__ int klen(const AttnParams& p, const Req& r, int mt) {
-    const int last = min(r.n, ((mt + 1) * BM - 1) / p.g + 1);
+    const int last = min(r.n, ((mt + 1) * p.bm - 1) / p.g + 1);
     return (int)r.ctx + last;
   }
   static __device__ __forceinline__ int row_tiles(const AttnParams& p, const Req& r) {
-    return (r.n * p.g + BM - 1) / BM;
+    return (r.n * p.g + p.bm - 1) / p.bm;
   }
   static __device__ long long head_units(const AttnParams& p, const Req& r) {
     const int nm = row_tiles(p, r);
@@ -111,9 +111,9 @@ __device__ __forceinline__ int block_of(const Share& s, long long u) {
 
 // Fills *out (shared memory); all NT threads call it. At least min_units go to
 // a block, so that pieces are not smaller than what joining them costs.
-template <int BM, int BK, int NT>
+template <int BK, int NT>
 __device__ void sched_begin(const AttnParams& p, int min_units, Share* out, long long* sums) {
-  typedef Sched<BM, BK> S;
+  typedef Sched<BK> S;
   const int tid = threadIdx.x;
   const int seg = (p.batch + NT - 1) / NT;
   const int b0 = tid * seg, b1 = min(p.batch, b0 + seg);
@@ -199,6 +199,15 @@ __device__ void attn_tail(const AttnParams& p) {
   }
 }
 
+// 1 / sum and the log-sum-exp of a row (maximum in log2 units): 0 and -inf for a
+// row that sees nothing, NaN where a score was
+__device__ __forceinline__ float inverse(float l) {
+  return l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+}
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l > 0.f ? (m + __log2f(l)) * kLn2 : (l == l ? neg_inf() : l);
+}
+
 __device__ __forceinline__ void store_out(float* p, float4 v) {
   *reinterpret_cast<float4*>(p) = v;
 }
@@ -217,8 +226,6 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnParams p) {
   pdl_wait();
   pdl_trigger();
   const int c = blockIdx.x;
-  if (p.fail && blockIdx.y == 0 && p.fail[c])
-    for (int b = threadIdx.x; b < p.batch; b += blockDim.x) atomicOr(p.status + b, PCT_DEV_TIMEOUT);
   const int4 m = p.meta[c];
   if (m.x < 0) return;
   const int b = m.x, h = m.y, mt = m.z, slot = m.w & 1, last = m.w >> 1;
@@ -250,7 +257,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnParams p) {
     }
     const int row = mt * BM + i, node = row / p.g, qh = h * p.g + row % p.g;
     const long long o = ((long long)b * p.n + node) * p.hq + qh;
-    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+    const float inv = inverse(l);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int d0 = j * 128 + lane * 4;
@@ -258,7 +265,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnParams p) {
         store_out(static_cast<T*>(p.out) + o * p.d + d0,
                   make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv));
     }
-    if (p.lse && lane == 0) p.lse[o] = l > 0.f ? (ref + __log2f(l)) * kLn2 : (l == l ? neg_inf() : l);
+    if (p.lse && lane == 0) p.lse[o] = lse_of(ref, l);
   }
 }
 

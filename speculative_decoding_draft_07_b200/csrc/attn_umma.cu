@@ -1,23 +1,28 @@
 // Tree attention for bf16 caches and many rows on the tcgen05 tensor cores.
 //
 // Above 64 rows (nodes x query heads of a group) the two products outweigh the
-// cache's bytes. One block an SM works on an item of up to 256 rows against key
-// tiles of 128 tokens as two streams of 128 rows (one thread a row):
-//   * warp 0: TMA producer. K and V tiles alternate through a ring of 128-byte
-//     swizzled slots, each page of a tile its own box (a lane a page);
-//   * warp 1, one thread: issues S_s = Q_s K^T (shared x shared) and
-//     O_s += P_s V (P_s from tensor memory) of whichever stream is ready, so one
-//     stream's products run under the other's softmax;
+// cache's bytes. One block an SM works on an item of two row tiles, R rows each
+// (R = the largest multiple of the group up to 128), against key tiles of 64 tokens,
+// as two streams:
+//   * warp 0: TMA producer. Publishes the items, loads their queries (double
+//     buffered) and streams K and V tiles through a ring of 128-byte swizzled
+//     slots, each page of a tile its own box (a lane a page);
+//   * warp 1, one thread: issues S = Q K^T (shared x shared) and O += P V (P from
+//     tensor memory) of whichever stream and step is ready. A stream's scores are
+//     double buffered, so its next S runs under the softmax of the current one;
 //   * warps 2-5 and 6-9: the softmax of stream 0 and 1. A thread reads its row of
-//     128 scores from tensor memory, keeps the running maximum and sum, and writes
+//     64 scores from tensor memory, keeps the running maximum and sum, and writes
 //     the weights back as bf16 over the scores.
-// With more than 128 rows in an item the streams are its two row tiles and share
+// With more than R rows in an item the streams are its two row tiles and share
 // every K and V tile; with fewer they take alternate key tiles of the same rows
 // and are added up at the item's end (both accumulators sit in the same tensor
-// memory lanes). Tensor memory: S_0, S_1 (128 columns each; P_s in the first 64
-// of S_s), O_0, O_1. The accumulator is rescaled only when a row's maximum grows by
-// more than 2^8 over the reference in use, which the later tiles seldom do;
-// weights up to 2^8 lose nothing in fp32 sums and bf16 products.
+// memory lanes). Tensor memory: S (2 streams x 2 buffers x 64 columns, P in the
+// first 32 of its S), then O_0, O_1. The accumulator is rescaled only when a row's
+// maximum grows by more than 2^8 over the reference in use, which the later tiles
+// seldom do; weights up to 2^8 lose nothing in fp32 sums and bf16 products.
+// 64 tokens a tile rather than 128: with 128 the scores fill tensor memory once
+// (head_dim 128), so that S, softmax and P V of a stream run one after another
+// (64 requests x 256 nodes over up to 4096 tokens: 1.41 ms).
 // Every mbarrier wait is bounded; when one gives up, the roles run to the end
 // without waiting, drain their copies and products, free the tensor memory, and
 // the join reports PCT_DEV_TIMEOUT.
@@ -31,22 +36,29 @@
 namespace pct {
 namespace {
 
-constexpr int UBM = 256;                 // rows of an item
-constexpr int UBK = 128;                 // tokens of a key tile
+constexpr int UBK = 64;                  // tokens of a key tile
 constexpr int UTHREADS = 320;
-constexpr int GONE = 4;                  // tiles whose bad-page marks are kept
+constexpr int UROWS = 256;               // row places of a piece (two streams of 128)
+constexpr int GONE = 8;                  // tiles whose bad-page marks are kept
+constexpr int ITEMS = 4;                 // published items
 
 template <int DP> struct UShape {
   static constexpr int HALVES = DP / 64;                   // 64-column boxes of a row
-  static constexpr int QTILE = 128 * DP * 2;
-  static constexpr int SLOT = UBK * DP * 2;
-  static constexpr int SLOTS = 4;
-  static constexpr size_t SMEM = 1024 + 2 * QTILE + SLOTS * SLOT;
+  static constexpr int QHALF = 128 * 128;                  // bytes of 128 rows of a box
+  static constexpr int QTILE = HALVES * QHALF;
+  static constexpr int KHALF = UBK * 128;
+  static constexpr int SLOT = HALVES * KHALF;
+  static constexpr int SLOTS = DP == 128 ? 6 : 8;          // K and V tiles in flight
+  // exchange of the streams' (maximum, sum): behind the staged half rows of a
+  // query buffer, or (one box a row) behind the ring
+  static constexpr int EXTRA = HALVES == 2 ? 0 : 2 * 128 * 8;
+  static constexpr size_t SMEM = 1024 + 4 * QTILE + SLOTS * SLOT + EXTRA;
 };
 
 struct UMaps {
-  int rows, shift;                       // tokens of a box (a page, at most 128), its log2
-  int slot_dim;                          // map axis of the token in a page: 1 or 2
+  int shift;                             // log2 of a box's tokens (a page, at most 64)
+  int slot_dim;                          // cache map axis of the token in a page: 1 or 2
+  int rows;                              // R
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y,
@@ -91,63 +103,43 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ void pair_sync() {   // both softmax groups
-  asm volatile("bar.sync 1, 256;" ::: "memory");
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// The items of a block's share, in order. seq numbers the key tiles that the
-// block loads (their ring slots follow from it).
-struct Walk {
-  long long u;
-  int b, h, mt, t0, t1, nt, rows, klen, seq, items;
-  bool split, first;
-  Req r;
-  __device__ void begin(const Share& s) {
-    u = s.u0; b = s.b; h = s.h; mt = s.mt; t0 = s.tile; t1 = t0; nt = 0;
-    seq = 0; items = 0; first = true; split = false;
-    r.n = 0;
-  }
-  __device__ bool next(const AttnParams& p, const Share& s) {
-    typedef Sched<UBM, UBK> S;
-    if (!first) {
-      seq += t1 - t0;
-      u += t1 - t0;
-      t0 = 0;
-      ++mt;
-      ++items;
-    }
-    if (u >= s.u1) return false;
-    if (first) r = attn_req(p, b);
-    first = false;
-    if (mt >= S::row_tiles(p, r)) { mt = 0; ++h; }
-    while (h >= p.hkv || r.n == 0) { ++b; h = 0; mt = 0; r = attn_req(p, b); }
-    klen = S::klen(p, r, mt);
-    nt = (klen + UBK - 1) / UBK;
-    t1 = (int)min((long long)nt, t0 + (s.u1 - u));
-    rows = min(UBM, r.n * p.g - mt * UBM);
-    split = rows <= 128;
-    return true;
-  }
-  // key tiles of stream st: first, and how many
+// An item as the producer publishes it. seq numbers the key tiles that the block
+// loads (their ring slots follow from it). The producer publishes item i only when
+// both softmax groups are done with item i - 2 (their query buffers are free), so
+// ITEMS entries need no hand-back.
+struct Item {
+  int b, h, mt, t0, t1, rows, klen, ctx, seq;
+  int last;                              // no more items; the rest is not set
+  int split;                             // streams on alternate tiles of the same rows
+  int whole, pslot;                      // written out directly, or the piece's slot
   __device__ int start(int st) const { return split ? t0 + st : t0; }
   __device__ int step() const { return split ? 2 : 1; }
 };
 
+// One accumulator column pair of 8: 16 bytes of a bf16 row.
+__device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
+  return make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+}
+
 template <int DP>
 __global__ void __launch_bounds__(UTHREADS, 1)
-attn_umma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                 const AttnParams p, const UMaps mp) {
+attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, const AttnParams p, const UMaps mp) {
   typedef UShape<DP> U;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sQ = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                           ~static_cast<uintptr_t>(1023));
-  uint8_t* ring = sQ + 2 * U::QTILE;
-  __shared__ uint64_t full[U::SLOTS], empty[U::SLOTS], qready[2], sfull[2], pready[2], pvdone[2],
-      drain;
+                                           ~static_cast<uintptr_t>(1023));   // [stream][2]
+  uint8_t* ring = sQ + 4 * U::QTILE;
+  __shared__ uint64_t full[U::SLOTS], empty[U::SLOTS], qfull[2][2], qempty[2][2], sfull[2][2],
+      pready[2][2], pvdone[2][2], item_full[ITEMS], pair, group[2], drain;
+  __shared__ Item items[ITEMS];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
-  __shared__ uint4 gone[GONE];
-  __shared__ float2 ml[2][128];
+  __shared__ uint2 gone[GONE];
   __shared__ Share share;
   __shared__ long long sums[UTHREADS / 32];
   volatile int* abort_flag = &abort_word;
@@ -157,16 +149,22 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   if (tid == 0) {
     for (int i = 0; i < U::SLOTS; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 2); }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&qready[i], 128);
-      mbar_init(&sfull[i], 1);
-      mbar_init(&pready[i], 128);
-      mbar_init(&pvdone[i], 1);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&qfull[i][j], 1);
+        mbar_init(&qempty[i][j], 128);
+        mbar_init(&sfull[i][j], 1);
+        mbar_init(&pready[i][j], 128);
+        mbar_init(&pvdone[i][j], 1);
+      }
+      mbar_init(&group[i], 128);
     }
+    for (int i = 0; i < ITEMS; ++i) mbar_init(&item_full[i], 1);
+    mbar_init(&pair, 256);
     mbar_init(&drain, 1);
     abort_word = 0;
     *err = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    fence_async_smem();
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -174,28 +172,81 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                  "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  sched_begin<UBM, UBK, UTHREADS>(p, 1, &share, sums);
+  sched_begin<UBK, UTHREADS>(p, 1, &share, sums);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
-  const uint32_t tS = tmem, tO = tmem + 256;
-  int4 begun = make_int4(-1, 0, 0, 0);
+  const uint32_t tS = tmem_slot, tO = tS + 256;
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
-    Walk w;
-    w.begin(share);
-    bool ok = true;
-    uint32_t armed = 0, armed_par = 0;
-    const int boxes = UBK >> mp.shift;              // boxes of a tile
-    while (ok && w.next(p, share)) {
-      const int32_t* table = p.table + (long long)w.b * p.max_pages;
-      for (int t = w.t0; t < w.t1 && ok; ++t) {
-        const int seq = w.seq + t - w.t0;
+    typedef Sched<UBK> S;
+    long long u = share.u0;
+    int b = share.b, h = share.h, mt = share.mt, t0 = share.tile, seq0 = 0, n_items = 0;
+    int4 begun = make_int4(-1, 0, 0, 0);
+    Req r;
+    r.n = 0;
+    bool ok = true, fresh = true;
+    uint32_t armed = 0;                              // ring slots used
+    int slot = 0;
+    uint32_t par = 0;
+    const int boxes = UBK >> mp.shift;               // boxes of a tile
+    const int nodes = mp.rows / p.g;                 // nodes of a row tile
+    while (ok) {
+      const bool end = u >= share.u1;
+      int klen = 0, nt = 0, t1 = t0, rows = 0;
+      if (!end) {
+        if (fresh) r = attn_req(p, b);
+        fresh = false;
+        if (mt >= S::row_tiles(p, r)) { mt = 0; ++h; }
+        while (h >= p.hkv || r.n == 0) { ++b; h = 0; mt = 0; r = attn_req(p, b); }
+        klen = S::klen(p, r, mt);
+        nt = (klen + UBK - 1) / UBK;
+        t1 = (int)min((long long)nt, t0 + (share.u1 - u));
+        rows = min(p.bm, r.n * p.g - mt * p.bm);
+      }
+      const int buf = n_items & 1;
+      const uint32_t qpar = (uint32_t)(n_items >> 1) & 1u;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        // the buffer's reader is done, and so is the copy before (a stream without
+        // tiles does not wait for its queries)
+        bool got = wait_bar(&qempty[s][buf], qpar ^ 1u, abort_flag, err);
+        if (n_items >= 2) got = got && wait_bar(&qfull[s][buf], qpar ^ 1u, abort_flag, err);
+        if (!__all_sync(0xffffffffu, got)) ok = false;
+      }
+      if (!ok) break;
+      const bool split = rows <= mp.rows;
+      if (lane == 0) {
+        Item& it = items[n_items % ITEMS];
+        it.b = b; it.h = h; it.mt = mt; it.t0 = t0; it.t1 = t1; it.rows = rows; it.klen = klen;
+        it.ctx = (int)r.ctx; it.seq = seq0; it.last = end; it.split = split;
+        it.whole = t0 == 0 && t1 == nt;
+        it.pslot = u == share.u0 ? 0 : 1;
+        if (!end && t0 == 0 && t1 < nt)
+          begun = make_int4(b, h, mt, it.pslot | block_of(share, u + nt - 1) << 1);
+        mbar_arrive(&item_full[n_items % ITEMS]);
+        if (!end) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            mbar_expect_tx(&qfull[s][buf], (uint32_t)(mp.rows * 128 * U::HALVES));
+            const int node = (mt * 2 + (split ? 0 : s)) * nodes;
+            const uint32_t dst = smem_u32(sQ + (s * 2 + buf) * U::QTILE);
+#pragma unroll
+            for (int hf = 0; hf < U::HALVES; ++hf)
+              tma_load_4d(dst + hf * U::QHALF, &tmQ, hf * 64, h * p.g, node, b, &qfull[s][buf]);
+          }
+        }
+      }
+      __syncwarp();
+      if (end) break;
+      ++n_items;
+      const int32_t* table = p.table + (long long)b * p.max_pages;
+      for (int t = t0; t < t1 && ok; ++t) {
+        const int seq = seq0 + t - t0;
         const int tok = t * UBK + (lane << mp.shift);
         int page = -1, place = 0;
-        const bool live = lane < boxes && tok < w.klen;
+        const bool live = lane < boxes && tok < klen;
         if (live) {
           const uint32_t col = page_of(p, tok);
           page = __ldg(table + col);
@@ -205,37 +256,43 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
         const uint32_t lost = __ballot_sync(0xffffffffu, live && page < 0);
         if (lane == 0) {
-          uint32_t g[4] = {0, 0, 0, 0};
+          uint32_t g[2] = {0, 0};
           for (int i = 0; lost >> i; ++i)
             if ((lost >> i) & 1)
               for (int k = i << mp.shift; k < (i + 1) << mp.shift; ++k) g[k >> 5] |= 1u << (k & 31);
-          gone[seq % GONE] = make_uint4(g[0], g[1], g[2], g[3]);
+          gone[seq % GONE] = make_uint2(g[0], g[1]);
         }
-        const uint32_t bytes = (uint32_t)__popc(have) * mp.rows * 128u * U::HALVES;
+        const uint32_t bytes = (uint32_t)__popc(have) * (128u << mp.shift) * U::HALVES;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          const int pos = seq * 2 + kv, slot = pos % U::SLOTS;
-          const uint32_t par = (uint32_t)(pos / U::SLOTS) & 1u;
           const bool got = wait_bar(&empty[slot], par ^ 1u, abort_flag, err);
           if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
           if (lane == 0) mbar_expect_tx(&full[slot], bytes);
           __syncwarp();
           if (page >= 0) {
-            const uint32_t dst = smem_u32(ring + slot * U::SLOT) + (uint32_t)(lane << mp.shift) * 128u;
-            const int y = mp.slot_dim == 1 ? place : w.h, z = mp.slot_dim == 1 ? w.h : place;
+            const uint32_t dst = smem_u32(ring + slot * U::SLOT) + ((uint32_t)lane << mp.shift) * 128u;
+            const int y = mp.slot_dim == 1 ? place : h, z = mp.slot_dim == 1 ? h : place;
 #pragma unroll
             for (int hf = 0; hf < U::HALVES; ++hf)
-              tma_load_4d(dst + hf * (UBK * 128), kv ? &tmV : &tmK, hf * 64, y, z, page, &full[slot]);
+              tma_load_4d(dst + hf * U::KHALF, kv ? &tmV : &tmK, hf * 64, y, z, page, &full[slot]);
           }
           armed |= 1u << slot;
-          armed_par = (armed_par & ~(1u << slot)) | (par << slot);
+          if (++slot == U::SLOTS) { slot = 0; par ^= 1u; }
         }
       }
+      seq0 += t1 - t0;
+      u += t1 - t0;
+      t0 = 0;
+      ++mt;
     }
-    // every copy has landed before the block may exit
+    if (lane == 0) p.meta[blockIdx.x] = begun;
+    // every copy has landed before the block may exit: slot i was last armed in the
+    // current round when i < slot, in the one before otherwise
 #pragma unroll
     for (int i = 0; i < U::SLOTS; ++i)
-      if (armed & (1u << i)) drain_wait(&full[i], (armed_par >> i) & 1u);
+      if (armed & (1u << i)) drain_wait(&full[i], i < slot ? par : par ^ 1u);
+    for (int i = max(0, n_items - 2); i < n_items; ++i)
+      for (int s = 0; s < 2; ++s) drain_wait(&qfull[s][i & 1], (uint32_t)(i >> 1) & 1u);
   } else if (warp == 1) {
     if (lane == 0) {
       // ---------------- products ----------------
@@ -244,74 +301,84 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
       constexpr uint32_t ID_PV = BASE | (1u << 16) | ((uint32_t)(DP >> 3) << 17);
       const uint64_t q_desc = make_desc(smem_u32(sQ), 16, 1024);
       const uint64_t k_desc = make_desc(smem_u32(ring), 16, 1024);
-      const uint64_t v_desc = make_desc(smem_u32(ring), UBK * 128, 1024);
-      Walk w[2];
-      int t[2], qk[2] = {0, 0}, pv[2] = {0, 0};     // tile in hand; products issued
-      bool live[2], turn[2] = {false, false};       // turn: S is out, P V is next
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        w[s].begin(share);
-        do {
-          live[s] = w[s].next(p, share);
-          t[s] = live[s] ? w[s].start(s) : 0;
-        } while (live[s] && t[s] >= w[s].t1);
-      }
-      long long t0 = clock64();
+      const uint64_t v_desc = make_desc(smem_u32(ring), U::KHALF, 1024);
+      // per stream: the item in hand, its next tile for S and its end; S and P V issued
+      int item[2] = {-1, -1}, t[2] = {0, 0}, t1[2] = {0, 0}, seq[2] = {0, 0}, step[2] = {1, 1};
+      int n_s[2] = {0, 0}, n_pv[2] = {0, 0};
+      // per stream and score buffer, of the P V to come: V's ring position << 2 | split << 1 | first
+      int todo0[2] = {0, 0}, todo1[2] = {0, 0};
+      bool head[2] = {true, true}, live[2] = {true, true};
+      long long c0 = 0;
       uint32_t spins = 0;
-      while (live[0] || live[1]) {
+      while (live[0] || live[1] || n_pv[0] < n_s[0] || n_pv[1] < n_s[1]) {
         bool moved = false;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (!live[s]) continue;
-          const int pos = (w[s].seq + t[s] - w[s].t0) * 2;
-          if (!turn[s]) {
-            const int slot = pos % U::SLOTS;
-            if (!mbar_test(&full[slot], (uint32_t)(pos / U::SLOTS) & 1u)) continue;
-            if (qk[s] > 0 && !mbar_test(&pvdone[s], (uint32_t)(pv[s] - 1) & 1u)) continue;
-            if (!mbar_test(&qready[s], (uint32_t)w[s].items & 1u)) continue;
-            tc_fence_after();
-            const uint64_t qd = q_desc + (uint64_t)((s * U::QTILE) >> 4);
-            const uint64_t kd = k_desc + (uint64_t)((slot * U::SLOT) >> 4);
+          if (n_pv[s] < n_s[s]) {                       // P V of the older tile
+            const int n = n_pv[s], bf = n & 1;
+            const int td = bf ? todo1[s] : todo0[s];
+            const int pos = td >> 2, slot = pos % U::SLOTS;
+            if (mbar_test(&pready[s][bf], (uint32_t)(n >> 1) & 1u) &&
+                mbar_test(&full[slot], (uint32_t)(pos / U::SLOTS) & 1u)) {
+              tc_fence_after();
+              const uint64_t vd = v_desc + (uint64_t)((slot * U::SLOT) >> 4);
+              const uint32_t more = !(td & 1);
 #pragma unroll
-            for (int k = 0; k < DP / 16; ++k) {
-              const uint64_t off = (uint64_t)(((k >> 2) * (UBK * 128) + (k & 3) * 32) >> 4);
-              umma_f16(tS + s * 128, qd + off, kd + off, ID_QK, k > 0);
-            }
-            umma_commit(&sfull[s]);
-            umma_commit(&empty[slot]);
-            if (w[s].split) umma_commit(&empty[slot]);
-            ++qk[s];
-            turn[s] = true;
-          } else {
-            const int slot = (pos + 1) % U::SLOTS;
-            if (!mbar_test(&pready[s], (uint32_t)pv[s] & 1u)) continue;
-            if (!mbar_test(&full[slot], (uint32_t)((pos + 1) / U::SLOTS) & 1u)) continue;
-            tc_fence_after();
-            const uint64_t vd = v_desc + (uint64_t)((slot * U::SLOT) >> 4);
-            const uint32_t more = t[s] != w[s].start(s);
-#pragma unroll
-            for (int k = 0; k < UBK / 16; ++k)
-              umma_ts(tO + s * DP, tS + s * 128 + k * 8, vd + (uint64_t)((k * 2048) >> 4), ID_PV,
-                      more | (k > 0));
-            umma_commit(&pvdone[s]);
-            umma_commit(&empty[slot]);
-            if (w[s].split) umma_commit(&empty[slot]);
-            ++pv[s];
-            turn[s] = false;
-            t[s] += w[s].step();
-            while (live[s] && t[s] >= w[s].t1) {
-              live[s] = w[s].next(p, share);
-              t[s] = live[s] ? w[s].start(s) : 0;
+              for (int k = 0; k < UBK / 16; ++k)
+                umma_ts(tO + s * DP, tS + s * 128 + bf * 64 + k * 8, vd + (uint64_t)((k * 2048) >> 4),
+                        ID_PV, more | (k > 0));
+              umma_commit(&pvdone[s][bf]);
+              umma_commit(&empty[slot]);
+              if (td & 2) umma_commit(&empty[slot]);    // the other stream does not use it
+              ++n_pv[s];
+              moved = true;
             }
           }
+          if (!live[s]) continue;
+          if (t[s] >= t1[s]) {                          // the next item
+            const int i = item[s] + 1;
+            if (!mbar_test(&item_full[i % ITEMS], (uint32_t)(i / ITEMS) & 1u)) continue;
+            const Item& it = items[i % ITEMS];
+            item[s] = i;
+            if (it.last) { live[s] = false; continue; }
+            t[s] = it.start(s);
+            t1[s] = it.t1;
+            step[s] = it.step();
+            seq[s] = it.seq - it.t0;
+            head[s] = true;
+            moved = true;
+            continue;
+          }
+          const int n = n_s[s], bf = n & 1;
+          if (n >= 2 && n_pv[s] < n - 1) continue;       // its buffer still waits for P V
+          const int pos = (seq[s] + t[s]) * 2, slot = pos % U::SLOTS;
+          if (!mbar_test(&full[slot], (uint32_t)(pos / U::SLOTS) & 1u)) continue;
+          if (n >= 2 && !mbar_test(&pvdone[s][bf], (uint32_t)((n >> 1) - 1) & 1u)) continue;
+          if (!mbar_test(&qfull[s][item[s] & 1], (uint32_t)(item[s] >> 1) & 1u)) continue;
+          tc_fence_after();
+          const uint64_t qd = q_desc + (uint64_t)(((s * 2 + (item[s] & 1)) * U::QTILE) >> 4);
+          const uint64_t kd = k_desc + (uint64_t)((slot * U::SLOT) >> 4);
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k)
+            umma_f16(tS + s * 128 + bf * 64,
+                     qd + (uint64_t)(((k >> 2) * U::QHALF + (k & 3) * 32) >> 4),
+                     kd + (uint64_t)(((k >> 2) * U::KHALF + (k & 3) * 32) >> 4), ID_QK, k > 0);
+          umma_commit(&sfull[s][bf]);
+          umma_commit(&empty[slot]);
+          if (step[s] == 2) umma_commit(&empty[slot]);
+          const int td = (pos + 1) << 2 | (step[s] == 2) << 1 | (head[s] ? 1 : 0);
+          if (bf) todo1[s] = td; else todo0[s] = td;
+          ++n_s[s];
+          head[s] = false;
+          t[s] += step[s];
           moved = true;
         }
         if (moved) {
           spins = 0;
         } else if ((++spins & 255u) == 0u) {
-          if (spins == 256u) t0 = clock64();
+          if (spins == 256u) c0 = clock64();
           if (*abort_flag) break;
-          if (clock64() - t0 > kTimeoutCycles) {
+          if (clock64() - c0 > kTimeoutCycles) {
             *abort_flag = 1;
             atomicExch(err, 1);
             break;
@@ -324,69 +391,55 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
   } else {
     // ---------------- softmax ----------------
     const int s = (warp - 2) >> 2, quad = warp & 3;
-    const int tl = (warp - 2 - s * 4) * 32 + lane;       // thread of the group
-    const int rr = quad * 32 + lane;                     // row of the stream = TMEM lane
+    const int tl = quad * 32 + lane;                     // thread of the group, row of the
+                                                         // stream, tensor memory lane
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
     const uint32_t aS = tS + s * 128 + lane_base, aO = tO + s * DP + lane_base;
     const float c = p.scale_log2;
-    uint8_t* myQ = sQ + s * U::QTILE;
-    int done = 0;                                        // tiles of this stream so far
+    int n = 0, n_items = 0;                              // tiles of this stream, items
+    uint32_t met = 0, met_group = 0;
     auto wait = [&](uint64_t* bar, uint32_t par) {
       const bool got = wait_bar(bar, par, abort_flag, err);
       return __all_sync(0xffffffffu, got);
     };
-    auto load_q = [&](const Walk& w) {
-      const int base = w.mt * UBM + (w.split ? 0 : s * 128), lim = w.rows - (w.split ? 0 : s * 128);
-      constexpr int CH = DP / 8;
-#pragma unroll 4
-      for (int i = 0; i < CH; ++i) {
-        const int r0 = (i * 128 + tl) / CH, ch = tl % CH;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r0 < lim && ch * 8 < p.d) {
-          const int row = base + r0, node = row / p.g, qh = w.h * p.g + (row - node * p.g);
-          x = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                   w.b * p.qs_b + node * p.qs_n + qh * p.qs_h +
-                                                   ch * 8));
-          x.x ^= p.q_sign; x.y ^= p.q_sign; x.z ^= p.q_sign; x.w ^= p.q_sign;
-        }
-        *reinterpret_cast<uint4*>(myQ + (ch >> 3) * (128 * 128) + r0 * 128 +
-                                  (((ch & 7) ^ (r0 & 7)) << 4)) = x;
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(&qready[s]);
+    auto pair_sync = [&]() {                             // both softmax groups (bounded)
+      mbar_arrive(&pair);
+      (void)wait(&pair, met++ & 1u);
     };
-
-    Walk w, nx;
-    nx.begin(share);
-    bool more = nx.next(p, share);
-    if (more) load_q(nx);
-    while (more) {
-      w = nx;
-      const int base = w.mt * UBM + (w.split ? 0 : s * 128), lim = w.rows - (w.split ? 0 : s * 128);
-      const int row = base + rr;
-      const bool valid = rr < lim;
-      const int node = valid ? row / p.g : -0x40000000;
+    auto group_sync = [&]() {                            // this one
+      mbar_arrive(&group[s]);
+      (void)wait(&group[s], met_group++ & 1u);
+    };
+    for (;; ++n_items) {
+      const int slot_i = n_items % ITEMS, buf = n_items & 1;
+      if (!wait(&item_full[slot_i], (uint32_t)(n_items / ITEMS) & 1u)) break;
+      const Item& w = items[slot_i];
+      if (w.last) break;
+      const bool split = w.split, whole = w.whole;
+      const int off = split ? 0 : s * mp.rows;           // the stream's first row of the item
+      const int lim = min(mp.rows, w.rows - off);
+      const int row0 = w.mt * p.bm + off;
+      const bool valid = tl < lim;
+      const int node = valid ? (row0 + tl) / p.g : -0x40000000;
       const uint32_t* words =
           p.mask && valid ? p.mask + ((long long)w.b * p.n + node) * p.words : nullptr;
-      const int ctx = (int)w.r.ctx;
+      const int ctx = w.ctx, seq0 = w.seq - w.t0, klen = w.klen, t1 = w.t1, step = w.step();
       float m = neg_inf(), l = 0.f;
-      bool any = false;
-      for (int t = w.start(s); t < w.t1; t += w.step()) {
-        const int seq = w.seq + t - w.t0, k0 = t * UBK;
-        (void)wait(&sfull[s], (uint32_t)done & 1u);
+      const int n0 = n;
+      for (int t = w.start(s); t < t1; t += step, ++n) {
+        const int seq = seq0 + t, k0 = t * UBK, bf = n & 1;
+        (void)wait(&sfull[s][bf], (uint32_t)(n >> 1) & 1u);
         tc_fence_after();
-        uint32_t x[128];
-        tmem_issue(aS, *reinterpret_cast<uint32_t(*)[64]>(&x[0]));
-        tmem_issue(aS + 64, *reinterpret_cast<uint32_t(*)[64]>(&x[64]));
-        const uint4 gq = *const_cast<const uint4*>(&gone[seq % GONE]);
-        const bool lost = (gq.x | gq.y | gq.z | gq.w) != 0;
-        tmem_wait(*reinterpret_cast<uint32_t(*)[64]>(&x[0]));
-        tmem_wait(*reinterpret_cast<uint32_t(*)[64]>(&x[64]));
+        uint32_t x[64];
+        __syncwarp();
+        tmem_issue(aS + bf * 64, x);
+        const uint2 gq = *const_cast<const uint2*>(&gone[seq % GONE]);
+        const bool lost = (gq.x | gq.y) != 0;
+        tmem_wait(x);
         if (k0 + UBK > ctx || lost) {                    // nodes, the end, or a bad page
-          const uint32_t g[4] = {gq.x, gq.y, gq.z, gq.w};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t bits = seen32(p, words, node, k0 + q * 32 - ctx) & ~g[q];
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t bits = seen32(p, words, node, k0 + q * 32 - ctx) & ~(q ? gq.y : gq.x);
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (!((bits >> j) & 1u)) x[q * 32 + j] = 0xff800000u;
@@ -394,17 +447,19 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
-        for (int j = 0; j < 128; j += 8)
+        for (int j = 0; j < 64; j += 8)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             mx[q] = fmax3(mx[q], __uint_as_float(x[j + 2 * q]), __uint_as_float(x[j + 2 * q + 1]));
         const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
         // a new reference when the old one is more than 2^8 behind
-        const bool move = mn > m && (m == neg_inf() || (mn - m) * c > 8.f);
-        if (__any_sync(0xffffffffu, move && any)) {
-          const float f = move && any ? (m == neg_inf() ? 0.f : ex2((m - mn) * c)) : 1.f;
+        const bool move = valid && mn > m && (m == neg_inf() || (mn - m) * c > 8.f);
+        if (n > n0 && __any_sync(0xffffffffu, move)) {
+          const float f = move ? (m == neg_inf() ? 0.f : ex2((m - mn) * c)) : 1.f;
           l *= f;
-          // S(t) is out, so this stream's earlier products are complete
+          // every product of this stream before P V of this tile is complete
+          (void)wait(&pvdone[s][bf ^ 1], (uint32_t)((n - 1) >> 1) & 1u);
+          tc_fence_after();
 #pragma unroll
           for (int j = 0; j < DP / 16; ++j) {
             uint32_t o[16];
@@ -422,7 +477,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         // the weights become bf16 (off by at most 2^-8 each, the product's operand
         // type); the sum is that of the fp32 values
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
           uint32_t o[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -432,208 +487,275 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             sum = f2_add(sum, e);
             o[j] = pack2(e.x, e.y);
           }
-          tmem_store16(aS + q * 16, o);
+          tmem_store16(aS + bf * 64 + q * 16, o);
         }
         l += sum.x + sum.y;
-        const int end = w.klen - k0;                     // tokens of the tile that exist
+        const int end = klen - k0;                       // tokens of the tile that exist
         if (end < UBK || lost) {
           // V rows that stand for no token: zero, so that 0 * V is 0
           const int pos = seq * 2 + 1, slot = pos % U::SLOTS;
           (void)wait(&full[slot], (uint32_t)(pos / U::SLOTS) & 1u);
-          const uint32_t g[4] = {gq.x, gq.y, gq.z, gq.w};
-          uint32_t mine = 0;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if ((tl >> 5) == q) mine = g[q];
-          if (tl >= end || ((mine >> (tl & 31)) & 1u)) {
+          if (tl < UBK && (tl >= end || (((tl < 32 ? gq.x : gq.y) >> (tl & 31)) & 1u))) {
             uint8_t* vr = ring + slot * U::SLOT + tl * 128;
 #pragma unroll
             for (int hf = 0; hf < U::HALVES; ++hf)
 #pragma unroll
               for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<uint4*>(vr + hf * (UBK * 128) + j * 16) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(vr + hf * U::KHALF + j * 16) = make_uint4(0, 0, 0, 0);
           }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          fence_async_smem();
         }
         tmem_store_wait();
         tc_fence_before();
-        mbar_arrive(&pready[s]);
-        any = true;
-        ++done;
+        mbar_arrive(&pready[s][bf]);
       }
-      // the next item's queries, while the last product runs
-      nx = w;
-      more = nx.next(p, share);
-      if (more) load_q(nx);
+      const bool any = n > n0;
       if (any) {
-        (void)wait(&pvdone[s], (uint32_t)(done - 1) & 1u);
+        (void)wait(&pvdone[s][(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u);
         tc_fence_after();
       }
-      const bool whole = w.t0 == 0 && w.t1 == w.nt;
-      const int pslot = w.u == share.u0 ? 0 : 1;
-      const int nd = valid ? node : 0;
-      const long long o_row = ((long long)w.b * p.n + nd) * p.hq + w.h * p.g + (row - nd * p.g);
-      const long long at = ((long long)blockIdx.x * 2 + pslot) * UBM + (w.split ? 0 : s * 128) + rr;
+      // O to the caller, through this item's query buffer (its products are complete)
+      // so that rows go out in full lines; pieces directly, [d / 4][row][4]
+      uint8_t* stage = sQ + (s * 2 + buf) * U::QTILE;
       const float ms = m == neg_inf() ? m : m * c;       // log2 units
-      if (!w.split) {
-        const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-        const float f = whole ? inv : 1.f;
+      const long long piece = (long long)blockIdx.x * 2 + w.pslot;
+      const int place = (split ? 0 : s * 128) + tl;
+      float4* po = reinterpret_cast<float4*>(p.po) + piece * (p.d / 4) * UROWS + place;
+      auto put = [&](int col, const float (&y)[8], int chunk) {   // 8 columns from `col`
+        if (whole) {
+          *reinterpret_cast<uint4*>(stage + (chunk >> 3) * U::QHALF + tl * 128 +
+                                    (((chunk & 7) ^ (tl & 7)) << 4)) = pack8(y);
+        } else if (valid && col < p.d) {
+          po[(col / 4) * UROWS] = make_float4(y[0], y[1], y[2], y[3]);
+          po[(col / 4 + 1) * UROWS] = make_float4(y[4], y[5], y[6], y[7]);
+        }
+      };
+      const int col0 = split ? s * (DP / 2) : 0, chunks = split ? DP / 16 : DP / 8;
+      (void)wait(&qfull[s][buf], (uint32_t)(n_items >> 1) & 1u);   // a stream without tiles
+      float row_m = ms, row_l = l;
+      if (!split) {
+        const float f = whole ? inverse(l) : 1.f;
 #pragma unroll
         for (int j = 0; j < DP / 16; ++j) {
           uint32_t o[16];
+          __syncwarp();
           tmem_issue(aO + j * 16, o);
           tmem_wait(o);
-          if (!valid || j * 16 >= p.d) continue;
 #pragma unroll
-          for (int q = 0; q < 16; q += 8) {
-            if (j * 16 + q >= p.d) continue;
+          for (int q = 0; q < 2; ++q) {
             float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(o[q + e]) * f;
-            if (whole) {
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o_row * p.d + j * 16 + q) =
-                  make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
-            } else {
-              float4* d4 = reinterpret_cast<float4*>(p.po + at * p.d + j * 16 + q);
-              d4[0] = make_float4(y[0], y[1], y[2], y[3]);
-              d4[1] = make_float4(y[4], y[5], y[6], y[7]);
-            }
+            for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(o[q * 8 + e]) * f;
+            put(j * 16 + q * 8, y, j * 2 + q);
           }
-        }
-        if (valid) {
-          if (!whole) p.pml[at] = make_float2(ms, l);
-          else if (p.lse) p.lse[o_row] = l > 0.f ? (ms + __log2f(l)) * kLn2 : (l == l ? neg_inf() : l);
         }
       } else {
         // the two streams hold the same rows: each group adds up half of the columns
-        ml[s][rr] = make_float2(ms, any ? l : 0.f);
+        auto ml = [&](int st) {
+          return reinterpret_cast<float2*>(U::EXTRA ? ring + U::SLOTS * U::SLOT + st * 128 * 8
+                                                    : sQ + (st * 2 + buf) * U::QTILE + U::QHALF) + tl;
+        };
+        *ml(s) = make_float2(ms, l);
         tc_fence_before();
         pair_sync();
         tc_fence_after();
-        const float2 a = ml[0][rr], b = ml[1][rr];
-        const float mx = fmaxf(a.x, b.x), ref = mx == neg_inf() ? 0.f : mx;
+        const float2 a = *ml(0), b = *ml(1);
+        row_m = fmaxf(a.x, b.x);
+        const float ref = row_m == neg_inf() ? 0.f : row_m;
         const float fa = ex2(a.x - ref), fb = ex2(b.x - ref);
-        const bool two = w.t1 - w.t0 > 1;                // stream 1 had a tile
-        const float sum = a.y * fa + (two ? b.y * fb : 0.f);
-        const float inv = sum > 0.f ? 1.f / sum : (sum == sum ? 0.f : sum);
-        const float f = whole ? inv : 1.f;
-        const uint32_t a0 = tO + lane_base;
+        const bool two = t1 - w.t0 > 1;                  // stream 1 had a tile
+        row_l = a.y * fa + b.y * fb;
+        const float f = whole ? inverse(row_l) : 1.f;
+        const uint32_t a0 = tO + lane_base + col0;
 #pragma unroll
-        for (int j2 = 0; j2 < DP / 32; ++j2) {
-          const int j = s * (DP / 32) + j2;
+        for (int j = 0; j < DP / 32; ++j) {
           uint32_t o[16], o2[16];
+          __syncwarp();
           tmem_issue(a0 + j * 16, o);
           tmem_issue(a0 + DP + j * 16, o2);
           tmem_wait(o);
           tmem_wait(o2);
-          if (!valid) continue;
 #pragma unroll
-          for (int q = 0; q < 16; q += 8) {
-            if (j * 16 + q >= p.d) continue;
+          for (int q = 0; q < 2; ++q) {
             float y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              y[e] = __uint_as_float(o[q + e]) * fa;
-              if (two) y[e] = fmaf(__uint_as_float(o2[q + e]), fb, y[e]);
+              y[e] = __uint_as_float(o[q * 8 + e]) * fa;
+              if (two) y[e] = fmaf(__uint_as_float(o2[q * 8 + e]), fb, y[e]);
               y[e] *= f;
             }
-            if (whole) {
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o_row * p.d + j * 16 + q) =
-                  make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
-            } else {
-              float4* d4 = reinterpret_cast<float4*>(p.po + at * p.d + j * 16 + q);
-              d4[0] = make_float4(y[0], y[1], y[2], y[3]);
-              d4[1] = make_float4(y[4], y[5], y[6], y[7]);
-            }
+            put(col0 + j * 16 + q * 8, y, j * 2 + q);
           }
-        }
-        if (valid && s == 0) {
-          if (!whole) p.pml[at] = make_float2(mx, sum);
-          else if (p.lse) p.lse[o_row] = sum > 0.f ? (ref + __log2f(sum)) * kLn2 : (sum == sum ? neg_inf() : sum);
         }
         tc_fence_before();
         pair_sync();                                     // both accumulators are read
         tc_fence_after();
       }
-      if (w.t0 == 0 && w.t1 < w.nt)
-        begun = make_int4(w.b, w.h, w.mt, pslot | block_of(share, w.u + w.nt - 1) << 1);
+      if (valid && !(split && s == 1)) {
+        if (!whole) p.pml[piece * UROWS + place] = make_float2(row_m, row_l);
+        else if (p.lse)
+          p.lse[((long long)w.b * p.n + node) * p.hq + w.h * p.g + (row0 + tl - node * p.g)] =
+              lse_of(row_m == neg_inf() ? 0.f : row_m, row_l);
+      }
+      if (whole) {
+        group_sync();
+        const int ch = tl % chunks, col = col0 + ch * 8;
+        for (int rr = tl / chunks; rr < lim; rr += 128 / chunks) {
+          const int row = row0 + rr, nd = row / p.g;
+          const long long o = ((long long)w.b * p.n + nd) * p.hq + w.h * p.g + (row - nd * p.g);
+          const uint4 y = *reinterpret_cast<const uint4*>(stage + (ch >> 3) * U::QHALF + rr * 128 +
+                                                          (((ch & 7) ^ (rr & 7)) << 4));
+          if (col < p.d)
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o * p.d + col) = y;
+        }
+      }
+      fence_async_smem();                                // the buffer's next writer is a copy
       tc_fence_before();
+      mbar_arrive(&qempty[s][buf]);
     }
-    if (warp == 2 && lane == 0) p.meta[blockIdx.x] = begun;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 1) {
     __syncwarp();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tS), "r"(512));
   }
   attn_tail<__nv_bfloat16>(p);
 }
 
-// [n_pages][heads][page places][d] as a 4D map; the place and the head in order of
-// their strides. Boxes of 64 columns x min(page, 128) places.
-bool encode_cache(CUtensorMap* map, const void* base, const AttnParams& p, int rows, int* slot_dim) {
+// Joins the pieces of the split item that block blockIdx.x began: a thread a row and
+// every fourth 4-column group, pieces in unit order.
+__global__ void __launch_bounds__(128) attn_umma_join_kernel(AttnParams p, int rows_tile) {
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x;
+  if (blockIdx.y == 0 && p.fail[c])
+    for (int b = threadIdx.x; b < p.batch; b += blockDim.x) atomicOr(p.status + b, PCT_DEV_TIMEOUT);
+  const int4 m = p.meta[c];
+  if (m.x < 0) return;
+  const int b = m.x, h = m.y, mt = m.z, slot = m.w & 1, last = m.w >> 1;
+  const Req r = attn_req(p, b);
+  const int rows = min(p.bm, r.n * p.g - mt * p.bm);
+  const int place = blockIdx.y * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+  const int s = place >> 7, rr = place & 127;
+  if (rr >= rows_tile || s * rows_tile + rr >= rows) return;
+  auto ml = [&](int k) { return p.pml[((long long)k * 2 + (k == c ? slot : 0)) * UROWS + place]; };
+  float mx = neg_inf();
+#pragma unroll 4
+  for (int k = c; k <= last; ++k) mx = fmaxf(mx, ml(k).x);
+  const float ref = mx == neg_inf() ? 0.f : mx;
+  const int d4 = p.d / 4;
+  float4 acc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 2
+  for (int k = c; k <= last; ++k) {
+    const float2 a = ml(k);
+    const float f = ex2(a.x - ref);
+    l = fmaf(a.y, f, l);
+    const float4* po = reinterpret_cast<const float4*>(p.po) +
+                       ((long long)k * 2 + (k == c ? slot : 0)) * d4 * UROWS + place;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (w + 4 * j < d4) {
+        const float4 x = po[(w + 4 * j) * UROWS];
+        acc[j].x = fmaf(x.x, f, acc[j].x); acc[j].y = fmaf(x.y, f, acc[j].y);
+        acc[j].z = fmaf(x.z, f, acc[j].z); acc[j].w = fmaf(x.w, f, acc[j].w);
+      }
+  }
+  const int row = mt * p.bm + s * rows_tile + rr, node = row / p.g;
+  const long long o = ((long long)b * p.n + node) * p.hq + h * p.g + (row - node * p.g);
+  const float inv = inverse(l);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (w + 4 * j < d4)
+      store_out(static_cast<__nv_bfloat16*>(p.out) + o * p.d + (w + 4 * j) * 4,
+                make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv));
+  if (p.lse && w == 0) p.lse[o] = lse_of(ref, l);
+}
+
+bool encode_4d(CUtensorMap* map, const void* base, const cuuint64_t (&dims)[4],
+               const cuuint64_t (&strides)[3], const cuuint32_t (&box)[4]) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  // an axis of one entry is never stepped over: any valid stride will do
-  const cuuint64_t row = (cuuint64_t)(p.d * 2 + 15) / 16 * 16;
-  const cuuint64_t slot = p.page_size > 1 ? (cuuint64_t)p.ks_slot * 2 : row;
-  const cuuint64_t head = p.hkv > 1 ? (cuuint64_t)p.ks_head * 2 : row;
-  const cuuint64_t page = p.n_pages > 1 ? (cuuint64_t)p.ks_page * 2 : std::max(slot, head);
-  *slot_dim = slot <= head ? 1 : 2;
-  const bool one = *slot_dim == 1;
-  const cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)(one ? p.page_size : p.hkv),
-                              (cuuint64_t)(one ? p.hkv : p.page_size), (cuuint64_t)p.n_pages};
-  const cuuint64_t strides[3] = {one ? slot : head, one ? head : slot, page};
-  const cuuint32_t box[4] = {64, one ? (cuuint32_t)rows : 1, one ? 1 : (cuuint32_t)rows, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
   for (int i = 0; i < 3; ++i)
     if (strides[i] == 0 || strides[i] >= (1ull << 40)) return false;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// [n_pages][heads][page places][d]; the place and the head in order of their strides.
+// Boxes of 64 columns x min(page, 64) places. (An axis of one entry is never
+// stepped over: any valid stride will do for it.)
+bool encode_cache(CUtensorMap* map, const void* base, const AttnParams& p, int rows, int* slot_dim) {
+  const cuuint64_t row = (cuuint64_t)(p.d * 2 + 15) / 16 * 16;
+  const cuuint64_t slot = p.page_size > 1 ? (cuuint64_t)p.ks_slot * 2 : row;
+  const cuuint64_t head = p.hkv > 1 ? (cuuint64_t)p.ks_head * 2 : row;
+  const cuuint64_t page = p.n_pages > 1 ? (cuuint64_t)p.ks_page * 2 : std::max(slot, head);
+  const bool one = slot <= head;
+  *slot_dim = one ? 1 : 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)(one ? p.page_size : p.hkv),
+                              (cuuint64_t)(one ? p.hkv : p.page_size), (cuuint64_t)p.n_pages};
+  const cuuint64_t strides[3] = {one ? slot : head, one ? head : slot, page};
+  const cuuint32_t box[4] = {64, one ? (cuuint32_t)rows : 1, one ? 1 : (cuuint32_t)rows, 1};
+  return encode_4d(map, base, dims, strides, box);
+}
+// [batch][n][heads][d], boxes of 64 columns x a group's heads x the nodes of a row tile
+bool encode_q(CUtensorMap* map, const AttnParams& p, int nodes) {
+  const cuuint64_t row = (cuuint64_t)(p.d * 2 + 15) / 16 * 16;
+  const cuuint64_t head = p.hq > 1 ? (cuuint64_t)p.qs_h * 2 : row;
+  const cuuint64_t node = p.n > 1 ? (cuuint64_t)p.qs_n * 2 : head;
+  const cuuint64_t req = p.batch > 1 ? (cuuint64_t)p.qs_b * 2 : node;
+  const cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)p.hq, (cuuint64_t)p.n, (cuuint64_t)p.batch};
+  const cuuint64_t strides[3] = {head, node, req};
+  const cuuint32_t box[4] = {64, (cuuint32_t)p.g, (cuuint32_t)nodes, 1};
+  return encode_4d(map, p.q, dims, strides, box);
+}
 
 template <int DP>
-cudaError_t run_umma(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v,
-                     const UMaps& mp, int grid, cudaStream_t s) {
+cudaError_t run_umma(const AttnParams& p, const CUtensorMap& q, const CUtensorMap& k,
+                     const CUtensorMap& v, const UMaps& mp, int grid, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(attn_umma_kernel<DP>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)UShape<DP>::SMEM);
   if (e != cudaSuccess) return e;
   {
     TraceScope t(s, "attn_umma");
-    attn_umma_kernel<DP><<<grid, UTHREADS, UShape<DP>::SMEM, s>>>(k, v, p, mp);
+    attn_umma_kernel<DP><<<grid, UTHREADS, UShape<DP>::SMEM, s>>>(q, k, v, p, mp);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
-  TraceScope t(s, "attn_join");
-  return launch_pdl(attn_join_kernel<__nv_bfloat16, UBM>, dim3(grid, UBM / 8), dim3(128), 0, s, 1, p);
+  TraceScope t(s, "attn_umma_join");
+  return launch_pdl(attn_umma_join_kernel, dim3(grid, UROWS / 32), dim3(128), 0, s, 1, p, mp.rows);
 }
 
 }  // namespace
 
-constexpr int kUmmaRows = UBM;
-int attn_umma_rows() { return kUmmaRows; }
+int attn_umma_rows() { return UROWS; }
 
-// Pages whose rows fill a swizzled tile without straddling it: a divisor of 128
-// from 8 rows (the swizzle's period) up, or a multiple of 128.
+// Pages whose rows fill a swizzled tile without straddling it: a divisor of 64
+// from 8 rows (the swizzle's period) up, or a multiple of 64.
 bool attn_umma_pages(int page_size) {
-  return page_size % 128 == 0 || (page_size >= 8 && 128 % page_size == 0);
+  return page_size % UBK == 0 || (page_size >= 8 && UBK % page_size == 0);
 }
 
-// PCT_EUNSUPPORTED-like: cudaErrorNotSupported when the cache cannot be mapped.
-cudaError_t launch_attn_umma(const AttnParams& p, int grid, cudaStream_t s) {
-  CUtensorMap k, v;
+// cudaErrorNotSupported when the strides do not fit a tensor map.
+cudaError_t launch_attn_umma(AttnParams p, int grid, cudaStream_t s) {
+  CUtensorMap q, k, v;
   UMaps mp;
-  mp.rows = p.page_size < 128 ? p.page_size : 128;
+  const int rows = std::min(p.page_size, UBK);
   mp.shift = 0;
-  while ((1 << mp.shift) < mp.rows) ++mp.shift;
-  if (!encode_cache(&k, p.k, p, mp.rows, &mp.slot_dim) ||
-      !encode_cache(&v, p.v, p, mp.rows, &mp.slot_dim))
+  while ((1 << mp.shift) < rows) ++mp.shift;
+  const int nodes = 128 / p.g;
+  mp.rows = nodes * p.g;
+  p.bm = 2 * mp.rows;
+  if (!encode_q(&q, p, nodes) || !encode_cache(&k, p.k, p, rows, &mp.slot_dim) ||
+      !encode_cache(&v, p.v, p, rows, &mp.slot_dim))
     return cudaErrorNotSupported;
-  return p.d <= 64 ? run_umma<64>(p, k, v, mp, grid, s) : run_umma<128>(p, k, v, mp, grid, s);
+  return p.d <= 64 ? run_umma<64>(p, q, k, v, mp, grid, s) : run_umma<128>(p, q, k, v, mp, grid, s);
 }
 
 }  // namespace pct

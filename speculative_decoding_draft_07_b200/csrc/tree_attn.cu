@@ -19,7 +19,7 @@ cudaError_t launch_attn_mma(const AttnParams& p, int bm, int grid, cudaStream_t 
 // attn_umma.cu
 int attn_umma_rows();
 bool attn_umma_pages(int page_size);
-cudaError_t launch_attn_umma(const AttnParams& p, int grid, cudaStream_t s);
+cudaError_t launch_attn_umma(AttnParams p, int grid, cudaStream_t s);
 
 namespace {
 
@@ -34,7 +34,7 @@ __device__ __forceinline__ float4 load4(const float* p) {
 template <int RPT, int DC>
 __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(AttnParams p) {
   constexpr int BM = 8 * RPT, BK = kSimtBK, NT = kSimtThreads;
-  typedef Sched<BM, BK> S;
+  typedef Sched<BK> S;
   extern __shared__ __align__(16) float sm[];
   __shared__ Share share;
   __shared__ long long sums[NT / 32];
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(AttnParams p) {
   float* Vs = Ks + BK * dp;                // [BK][dp]
   float* Ps = Vs + BK * dp;                // [BK][BM]
   const int tid = threadIdx.x, rg = tid >> 4, cg = tid & 15;
-  sched_begin<BM, BK, NT>(p, 2, &share, sums);
+  sched_begin<BK, NT>(p, 2, &share, sums);
   int4 begun = make_int4(-1, 0, 0, 0);
 
   long long u = share.u0;
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(AttnParams p) {
       if (whole) {
         const int row = row0 + rr, node = row / p.g, qh = h * p.g + (row - node * p.g);
         const long long o = ((long long)b * p.n + node) * p.hq + qh;
-        const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == l[i] ? 0.f : l[i]);
+        const float inv = inverse(l[i]);
 #pragma unroll
         for (int q = 0; q < DC / 4; ++q) {
           const int c = q * 64 + cg * 4;
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(AttnParams p) {
                                   acc[i][q * 4 + 2] * inv, acc[i][q * 4 + 3] * inv));
         }
         if (p.lse && cg == 0)
-          p.lse[o] = l[i] > 0.f ? (m[i] + __log2f(l[i])) * kLn2 : (l[i] == l[i] ? neg_inf() : l[i]);
+          p.lse[o] = lse_of(m[i], l[i]);
       } else {
         const long long at = ((long long)blockIdx.x * 2 + slot) * BM + rr;
 #pragma unroll
@@ -301,12 +301,11 @@ cudaError_t launch_attn(const AttnArgs& a, void* ws, cudaStream_t s) {
   p.pml = reinterpret_cast<float2*>(w + P.o_ml);
   p.meta = reinterpret_cast<int4*>(w + P.o_meta);
   p.fail = nullptr;
-  p.q_sign = 0;
-  // scale 0 stays off the tcgen05 kernel, which scales masked (-inf) scores
-  if (P.umma && a.scale != 0.f) {
+  p.bm = P.bm;
+  // the tcgen05 kernel scales masked (-inf) scores and takes maxima before scaling
+  if (P.umma && a.scale > 0.f) {
     AttnParams up = p;
     up.fail = reinterpret_cast<int32_t*>(w + P.o_fail);
-    if (a.scale < 0.f) { up.scale_log2 = -p.scale_log2; up.q_sign = 0x80008000u; }
     const cudaError_t e = launch_attn_umma(up, num_sms(), s);
     if (e != cudaErrorNotSupported) return e;   // strides a tensor map cannot hold: the other kernel
   }
