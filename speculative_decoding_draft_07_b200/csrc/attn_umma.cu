@@ -7,10 +7,13 @@
 //   * warp 0: TMA producer. Publishes the items, loads their queries (double
 //     buffered) and streams K and V tiles through a ring of 128-byte swizzled
 //     slots, each page of a tile its own box (a lane a page);
-//   * warp 1, one thread: issues S = Q K^T (shared x shared) and O += P V (P from
-//     tensor memory) of whichever stream and step is ready. A stream's scores are
-//     double buffered, so its next S runs under the softmax of the current one;
-//   * warps 2-5 and 6-9: the softmax of stream 0 and 1. A thread reads its row of
+//   * warps 1 and 2, one thread each: issue S = Q K^T (shared x shared) and O += P V
+//     (P from tensor memory) of stream 0 and 1. A stream's scores are double
+//     buffered, so its next S runs under the softmax of the current one. Two
+//     issuers because issuing blocks while products run and each change between
+//     the two kinds costs an issuer about 150 cycles: one thread for both streams
+//     takes 1768 cycles for 128 tokens of a stream, two threads 1269;
+//   * warps 3-6 and 7-10: the softmax of stream 0 and 1. A thread reads its row of
 //     64 scores from tensor memory, keeps the running maximum and sum, and writes
 //     the weights back as bf16 over the scores.
 // With more than R rows in an item the streams are its two row tiles and share
@@ -37,7 +40,7 @@ namespace pct {
 namespace {
 
 constexpr int UBK = 64;                  // tokens of a key tile
-constexpr int UTHREADS = 320;
+constexpr int UTHREADS = 352;
 constexpr int UROWS = 256;               // row places of a piece (two streams of 128)
 constexpr int GONE = 8;                  // tiles whose bad-page marks are kept
 constexpr int ITEMS = 4;                 // published items
@@ -135,7 +138,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                                            ~static_cast<uintptr_t>(1023));   // [stream][2]
   uint8_t* ring = sQ + 4 * U::QTILE;
   __shared__ uint64_t full[U::SLOTS], empty[U::SLOTS], qfull[2][2], qempty[2][2], sfull[2][2],
-      pready[2][2], pvdone[2][2], item_full[ITEMS], pair, group[2], drain;
+      pready[2][2], pvdone[2][2], item_full[ITEMS], pair, group[2], drain[2];
   __shared__ Item items[ITEMS];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
@@ -157,10 +160,10 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         mbar_init(&pvdone[i][j], 1);
       }
       mbar_init(&group[i], 128);
+      mbar_init(&drain[i], 1);
     }
     for (int i = 0; i < ITEMS; ++i) mbar_init(&item_full[i], 1);
     mbar_init(&pair, 256);
-    mbar_init(&drain, 1);
     abort_word = 0;
     *err = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -293,85 +296,85 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       if (armed & (1u << i)) drain_wait(&full[i], i < slot ? par : par ^ 1u);
     for (int i = max(0, n_items - 2); i < n_items; ++i)
       for (int s = 0; s < 2; ++s) drain_wait(&qfull[s][i & 1], (uint32_t)(i >> 1) & 1u);
-  } else if (warp == 1) {
+  } else if (warp <= 2) {
     if (lane == 0) {
-      // ---------------- products ----------------
+      // ---------------- products of stream s ----------------
       constexpr uint32_t BASE = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
       constexpr uint32_t ID_QK = BASE | ((uint32_t)(UBK >> 3) << 17);
       constexpr uint32_t ID_PV = BASE | (1u << 16) | ((uint32_t)(DP >> 3) << 17);
-      const uint64_t q_desc = make_desc(smem_u32(sQ), 16, 1024);
+      const int s = warp - 1;
+      const uint64_t q_desc = make_desc(smem_u32(sQ + s * 2 * U::QTILE), 16, 1024);
       const uint64_t k_desc = make_desc(smem_u32(ring), 16, 1024);
       const uint64_t v_desc = make_desc(smem_u32(ring), U::KHALF, 1024);
-      // per stream: the item in hand, its next tile for S and its end; S and P V issued
-      int item[2] = {-1, -1}, t[2] = {0, 0}, t1[2] = {0, 0}, seq[2] = {0, 0}, step[2] = {1, 1};
-      int n_s[2] = {0, 0}, n_pv[2] = {0, 0};
-      // per stream and score buffer, of the P V to come: V's ring position << 2 | split << 1 | first
-      int todo0[2] = {0, 0}, todo1[2] = {0, 0};
-      bool head[2] = {true, true}, live[2] = {true, true};
+      // the item in hand, its next tile for S and its end; S and P V issued
+      int item = -1, t = 0, t1 = 0, seq = 0, step = 1, n_s = 0, n_pv = 0;
+      // per score buffer, of the P V to come: V's ring position << 2 | split << 1 | first
+      int todo0 = 0, todo1 = 0;
+      bool head = true, live = true;
       long long c0 = 0;
       uint32_t spins = 0;
-      while (live[0] || live[1] || n_pv[0] < n_s[0] || n_pv[1] < n_s[1]) {
+      while (live || n_pv < n_s) {
+        // the P V of the older tile where its weights are there, else the next S;
+        // neither waits for the other (the next item may need this P V)
         bool moved = false;
+        if (n_pv < n_s) {
+          const int bf = n_pv & 1, td = bf ? todo1 : todo0;
+          const int pos = td >> 2, slot = pos % U::SLOTS;
+          if (mbar_test(&pready[s][bf], (uint32_t)(n_pv >> 1) & 1u) &&
+              mbar_test(&full[slot], (uint32_t)(pos / U::SLOTS) & 1u)) {
+            tc_fence_after();
+            const uint64_t vd = v_desc + (uint64_t)((slot * U::SLOT) >> 4);
+            const uint32_t more = !(td & 1);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (n_pv[s] < n_s[s]) {                       // P V of the older tile
-            const int n = n_pv[s], bf = n & 1;
-            const int td = bf ? todo1[s] : todo0[s];
-            const int pos = td >> 2, slot = pos % U::SLOTS;
-            if (mbar_test(&pready[s][bf], (uint32_t)(n >> 1) & 1u) &&
-                mbar_test(&full[slot], (uint32_t)(pos / U::SLOTS) & 1u)) {
-              tc_fence_after();
-              const uint64_t vd = v_desc + (uint64_t)((slot * U::SLOT) >> 4);
-              const uint32_t more = !(td & 1);
-#pragma unroll
-              for (int k = 0; k < UBK / 16; ++k)
-                umma_ts(tO + s * DP, tS + s * 128 + bf * 64 + k * 8, vd + (uint64_t)((k * 2048) >> 4),
-                        ID_PV, more | (k > 0));
-              umma_commit(&pvdone[s][bf]);
-              umma_commit(&empty[slot]);
-              if (td & 2) umma_commit(&empty[slot]);    // the other stream does not use it
-              ++n_pv[s];
-              moved = true;
-            }
-          }
-          if (!live[s]) continue;
-          if (t[s] >= t1[s]) {                          // the next item
-            const int i = item[s] + 1;
-            if (!mbar_test(&item_full[i % ITEMS], (uint32_t)(i / ITEMS) & 1u)) continue;
-            const Item& it = items[i % ITEMS];
-            item[s] = i;
-            if (it.last) { live[s] = false; continue; }
-            t[s] = it.start(s);
-            t1[s] = it.t1;
-            step[s] = it.step();
-            seq[s] = it.seq - it.t0;
-            head[s] = true;
+            for (int k = 0; k < UBK / 16; ++k)
+              umma_ts(tO + s * DP, tS + s * 128 + bf * 64 + k * 8, vd + (uint64_t)((k * 2048) >> 4),
+                      ID_PV, more | (k > 0));
+            umma_commit(&pvdone[s][bf]);
+            umma_commit(&empty[slot]);
+            if (td & 2) umma_commit(&empty[slot]);      // the other stream does not use it
+            ++n_pv;
             moved = true;
-            continue;
           }
-          const int n = n_s[s], bf = n & 1;
-          if (n >= 2 && n_pv[s] < n - 1) continue;       // its buffer still waits for P V
-          const int pos = (seq[s] + t[s]) * 2, slot = pos % U::SLOTS;
-          if (!mbar_test(&full[slot], (uint32_t)(pos / U::SLOTS) & 1u)) continue;
-          if (n >= 2 && !mbar_test(&pvdone[s][bf], (uint32_t)((n >> 1) - 1) & 1u)) continue;
-          if (!mbar_test(&qfull[s][item[s] & 1], (uint32_t)(item[s] >> 1) & 1u)) continue;
-          tc_fence_after();
-          const uint64_t qd = q_desc + (uint64_t)(((s * 2 + (item[s] & 1)) * U::QTILE) >> 4);
-          const uint64_t kd = k_desc + (uint64_t)((slot * U::SLOT) >> 4);
+        }
+        if (live && t >= t1) {                          // the next item
+          const int i = item + 1;
+          if (mbar_test(&item_full[i % ITEMS], (uint32_t)(i / ITEMS) & 1u)) {
+            const Item& it = items[i % ITEMS];
+            item = i;
+            if (it.last) {
+              live = false;
+            } else {
+              t = it.start(s);
+              t1 = it.t1;
+              step = it.step();
+              seq = it.seq - it.t0;
+              head = true;
+            }
+            moved = true;
+          }
+        } else if (live && n_s - n_pv < 2) {
+          const int bf = n_s & 1, pos = (seq + t) * 2, slot = pos % U::SLOTS;
+          if (mbar_test(&full[slot], (uint32_t)(pos / U::SLOTS) & 1u) &&
+              (n_s < 2 || mbar_test(&pvdone[s][bf], (uint32_t)((n_s >> 1) - 1) & 1u)) &&
+              mbar_test(&qfull[s][item & 1], (uint32_t)(item >> 1) & 1u)) {
+            tc_fence_after();
+            const uint64_t qd = q_desc + (uint64_t)(((item & 1) * U::QTILE) >> 4);
+            const uint64_t kd = k_desc + (uint64_t)((slot * U::SLOT) >> 4);
 #pragma unroll
-          for (int k = 0; k < DP / 16; ++k)
-            umma_f16(tS + s * 128 + bf * 64,
-                     qd + (uint64_t)(((k >> 2) * U::QHALF + (k & 3) * 32) >> 4),
-                     kd + (uint64_t)(((k >> 2) * U::KHALF + (k & 3) * 32) >> 4), ID_QK, k > 0);
-          umma_commit(&sfull[s][bf]);
-          umma_commit(&empty[slot]);
-          if (step[s] == 2) umma_commit(&empty[slot]);
-          const int td = (pos + 1) << 2 | (step[s] == 2) << 1 | (head[s] ? 1 : 0);
-          if (bf) todo1[s] = td; else todo0[s] = td;
-          ++n_s[s];
-          head[s] = false;
-          t[s] += step[s];
-          moved = true;
+            for (int k = 0; k < DP / 16; ++k)
+              umma_f16(tS + s * 128 + bf * 64,
+                       qd + (uint64_t)(((k >> 2) * U::QHALF + (k & 3) * 32) >> 4),
+                       kd + (uint64_t)(((k >> 2) * U::KHALF + (k & 3) * 32) >> 4), ID_QK, k > 0);
+            umma_commit(&sfull[s][bf]);
+            umma_commit(&empty[slot]);
+            if (step == 2) umma_commit(&empty[slot]);
+            const int td = (pos + 1) << 2 | (step == 2) << 1 | (head ? 1 : 0);
+            if (bf) todo1 = td; else todo0 = td;
+            ++n_s;
+            head = false;
+            t += step;
+            moved = true;
+          }
         }
         if (moved) {
           spins = 0;
@@ -385,12 +388,12 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           }
         }
       }
-      umma_commit(&drain);
-      drain_wait(&drain, 0);
+      umma_commit(&drain[s]);
+      drain_wait(&drain[s], 0);
     }
   } else {
     // ---------------- softmax ----------------
-    const int s = (warp - 2) >> 2, quad = warp & 3;
+    const int s = (warp - 3) >> 2, quad = warp & 3;
     const int tl = quad * 32 + lane;                     // thread of the group, row of the
                                                          // stream, tensor memory lane
     const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
