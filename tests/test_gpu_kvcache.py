@@ -173,6 +173,33 @@ def test_keys_of_unseen_nodes_do_not_enter(n, hq, bad):
     assert torch.equal(r.out, want) and torch.equal(r.lse, wl)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,hq", [(1, 8), (60, 8), (100, 32)])
+def test_non_finite_keys_that_are_seen(n, hq, dtype):
+    """A NaN in a context key makes every row that sees it NaN, and only those; where every key a row
+    sees scores -inf the row is empty; one key at -inf has no weight."""
+    c = _case(13, dtype=dtype, n=n, hq=hq, ctx=(70, 70, 70, 70), d=64)
+    g, table, ctx, counts, m = c
+    g["q"] = g["q"].abs() + 0.5
+    clean = _run(g)
+    torch.cuda.synchronize()
+    want, wl = clean.out.clone(), clean.lse.clone()
+    at = lambda b, t: (int(table[b, t // 16]), t % 16)       # noqa: E731
+    g["k"][at(0, 40)][..., 3] = float("nan")
+    for t in range(ctx[1] + counts[1]):
+        g["k"][at(1, t)] = float("-inf")
+    g["k"][at(2, 69)] = float("-inf")
+    r = _run(g)
+    torch.cuda.synchronize()
+    assert torch.isnan(r.out[0]).all() and torch.isnan(r.lse[0]).all()
+    assert (r.out[1] == 0).all() and torch.isneginf(r.lse[1]).all()
+    # leaving out weight p lowers the lse by -ln(1 - p), which vanishes in fp32 for p < 2^-24; each side
+    # is off by at most 256 steps of 2^-24 besides (the sums' order may differ)
+    assert torch.isfinite(r.out[2].float()).all() and (r.lse[2] <= wl[2] + 2.0 ** -16).all()
+    assert (r.lse[2] < wl[2]).any()
+    assert torch.equal(r.out[3], want[3]) and torch.equal(r.lse[3], wl[3])
+
+
 def test_large_scores_and_a_given_scale():
     """Scores far from 0 and a scale that is not 1 / sqrt(d), negative too."""
     for scale in (1.0, -0.7, 3e-3):
