@@ -63,7 +63,6 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<DP>::MINB) attn_mma_kern
   constexpr int CH = DP / 8;                           // 16-byte pieces a row
   constexpr int STAGES = MmaShape<DP>::STAGES, TILE = MmaShape<DP>::TILE;
   constexpr bool QREG = DP <= 128;                     // Q fragments stay in registers
-  typedef Sched<BK> S;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Share share;
   __shared__ long long sums[NT / 32];
@@ -74,19 +73,15 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<DP>::MINB) attn_mma_kern
   float* obuf = reinterpret_cast<float*>(ring);        // [WK][BM][DP + 8] at an item's end
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wm = warp % WM, wk = warp / WM;
   if (tid < STAGES) gone[tid] = 0;
-  sched_begin<BK, NT>(p, 1, &share, sums);
+  sched_begin<BK, NT>(p, &share, sums);
   int4 begun = make_int4(-1, 0, 0, 0);
 
-  long long u = share.u0;
-  int b = share.b, h = share.h, mt = share.mt, t0 = share.tile;
-  while (u < share.u1) {
-    Req r = attn_req(p, b);
-    const int nm = S::row_tiles(p, r);
-    if (mt >= nm) { mt = 0; ++h; }
-    while (h >= p.hkv || r.n == 0) { ++b; h = 0; mt = 0; r = attn_req(p, b); }
-    const int klen = S::klen(p, r, mt), nt = (klen + BK - 1) / BK;
-    const int t1 = (int)min((long long)nt, t0 + (share.u1 - u));
-    const int row0 = mt * BM, rows = min(BM, r.n * p.g - row0);
+  Walk<BK> w;
+  w.begin(share);
+  while (w.next(p, share, &begun)) {
+    const Req r = w.r;
+    const int b = w.b, h = w.h, t0 = w.t0, t1 = w.t1, klen = w.klen, rows = w.rows;
+    const int row0 = (w.mt - 1) * BM;
     const int ctx = (int)r.ctx;
     const int32_t* table = p.table + (long long)b * p.max_pages;
     const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(p.k) + h * p.ks_head;
@@ -288,8 +283,8 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<DP>::MINB) attn_mma_kern
         *reinterpret_cast<float2*>(o + j * 8) = make_float2(acc[j][2 * i] * f, acc[j][2 * i + 1] * f);
     }
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == nt;
-    const int slot = u == share.u0 ? 0 : 1;
+    const bool whole = w.whole;
+    const int slot = w.pslot;
     const int v4 = p.d / 4;
     for (int i = tid; i < rows * v4; i += NT) {
       const int rr = i / v4, c = (i - rr * v4) * 4;
@@ -318,11 +313,6 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<DP>::MINB) attn_mma_kern
         if (c == 0) p.pml[at] = make_float2(mx, sum);
       }
     }
-    if (t0 == 0 && t1 < nt)
-      begun = make_int4(b, h, mt, slot | block_of(share, u + nt - 1) << 1);
-    u += t1 - t0;
-    t0 = 0;
-    ++mt;
   }
   if (tid == 0) p.meta[blockIdx.x] = begun;
   attn_tail<__nv_bfloat16>(p);

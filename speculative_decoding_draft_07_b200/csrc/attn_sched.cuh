@@ -2,10 +2,10 @@
 //
 // An item is (request b, kv head h, row tile mt): up to bm rows (node, query
 // head of the group) against klen = ctx_len + (last node of the tile + 1)
-// tokens, in ceil(klen / BK) key tiles. The units (key tiles of all items in
-// order) are divided evenly over the grid, so lengths from one token to the
-// longest balance without the host knowing them: a block's share may begin and
-// end inside items. An item inside one share is written out directly; the
+// tokens, in ceil(klen / BK) key tiles. Items and tiles have costs in units; the
+// units of all items in order are divided evenly over the grid, so lengths from
+// one token to the longest balance without the host knowing them: a block's share
+// may begin and end inside items (a tile goes where its first unit is). An item inside one share is written out directly; the
 // pieces of a split item go to the workspace as (unnormalised fp32 sums, row
 // maximum, row sum), at most two a block (slot 0: the share's first item, slot
 // 1: its last), and the join kernel adds them up in unit order, so results do
@@ -33,6 +33,8 @@ struct AttnParams {
   float2* pml;                  // [grid][2][bm] pieces' (maximum in log2 units, sum)
   int32_t* fail;                // [grid] set by a block whose bounded wait gave up (attn_umma)
   int bm;                       // rows of an item
+  int half;                     // units: `few` a tile of an item with at most this many
+  int few, many, per_item;      // rows, `many` of one with more, `per_item` an item
   uint32_t pg_mul, pg_shift;    // t / page_size = (umulhi(t, mul) + t) >> shift
   int4* meta;                   // [grid] split item begun by the block: b (-1 none),
                                 // h, mt, slot | last block << 1
@@ -93,26 +95,76 @@ struct Sched {
   static __device__ long long head_units(const AttnParams& p, const Req& r) {
     const int nm = row_tiles(p, r);
     long long s = 0;
-    for (int mt = 0; mt < nm; ++mt) s += (klen(p, r, mt) + BK - 1) / BK;
+    for (int mt = 0; mt < nm; ++mt) s += item_units(p, r, mt);
     return s;
+  }
+  static __device__ __forceinline__ int tiles(const AttnParams& p, const Req& r, int mt) {
+    return (klen(p, r, mt) + BK - 1) / BK;
+  }
+  static __device__ __forceinline__ int weight(const AttnParams& p, const Req& r, int mt) {
+    return min(p.bm, r.n * p.g - mt * p.bm) > p.half ? p.many : p.few;
+  }
+  static __device__ __forceinline__ int item_units(const AttnParams& p, const Req& r, int mt) {
+    return tiles(p, r, mt) * weight(p, r, mt) + p.per_item;
   }
 };
 
-// A block's place in the schedule. cur_* is the item of the next unit.
+// A block's place in the schedule: its units, and the item of the first one.
 struct Share {
-  long long u0, u1;             // units of this block
+  long long u0, u1;
   long long total, per, extra;  // per (+ 1 for the first `extra` blocks) units a block
-  int b, h, mt, tile;
+  int b, h, mt, off;            // off: units of the item before u0
 };
 __device__ __forceinline__ int block_of(const Share& s, long long u) {
   const long long cut = s.extra * (s.per + 1);
   return (int)(u < cut ? u / (s.per + 1) : s.extra + (u - cut) / s.per);
 }
 
-// Fills *out (shared memory); all NT threads call it. At least min_units go to
-// a block, so that pieces are not smaller than what joining them costs.
+// The walk over a share's items. All threads of a role take the same steps.
+template <int BK>
+struct Walk {
+  typedef Sched<BK> S;
+  long long u;
+  int b, h, mt, off;
+  Req r;
+  bool fresh;
+  // of the item in hand: its key tiles t0 .. t1 - 1 of nt here, rows, tokens; whether
+  // that is all of it; the piece's slot where not; the join's note where it begins here
+  int t0, t1, nt, rows, klen, pslot;
+  bool whole;
+  __device__ __forceinline__ void begin(const Share& s) {
+    u = s.u0; b = s.b; h = s.h; mt = s.mt; off = s.off; fresh = true;
+  }
+  __device__ __forceinline__ bool next(const AttnParams& p, const Share& s, int4* begun) {
+    while (u < s.u1) {
+      if (fresh) r = attn_req(p, b);
+      fresh = false;
+      if (mt >= S::row_tiles(p, r)) { mt = 0; ++h; }
+      while (h >= p.hkv || r.n == 0) { ++b; h = 0; mt = 0; r = attn_req(p, b); }
+      klen = S::klen(p, r, mt);
+      nt = (klen + BK - 1) / BK;
+      const int w = S::weight(p, r, mt);
+      // the item's own units come first, then its tiles'
+      const int c = p.per_item, e = (int)min((long long)nt * w + c, off + (s.u1 - u));
+      t0 = (max(off - c, 0) + w - 1) / w;
+      t1 = (max(e - c, 0) + w - 1) / w;
+      rows = min(p.bm, r.n * p.g - mt * p.bm);
+      whole = t0 == 0 && t1 == nt;
+      pslot = u == s.u0 ? 0 : 1;
+      if (t0 == 0 && t1 > 0 && t1 < nt)
+        *begun = make_int4(b, h, mt, pslot | block_of(s, u - off + c + (long long)(nt - 1) * w) << 1);
+      u += e - off;
+      off = 0;
+      ++mt;                      // (b, h, mt - 1) is the item in hand
+      if (t0 < t1) return true;
+    }
+    return false;
+  }
+};
+
+// Fills *out (shared memory); all NT threads call it.
 template <int BK, int NT>
-__device__ void sched_begin(const AttnParams& p, int min_units, Share* out, long long* sums) {
+__device__ void sched_begin(const AttnParams& p, Share* out, long long* sums) {
   typedef Sched<BK> S;
   const int tid = threadIdx.x;
   const int seg = (p.batch + NT - 1) / NT;
@@ -138,7 +190,7 @@ __device__ void sched_begin(const AttnParams& p, int min_units, Share* out, long
     total += sums[k];
   }
   const long long ex = base + inc - mine;
-  long long blocks = (total + min_units - 1) / min_units;
+  long long blocks = total / max(p.few, p.many);   // a whole tile at least in every part of an item
   if (blocks > gridDim.x) blocks = gridDim.x;
   if (blocks < 1) blocks = 1;
   const long long per = total / blocks, extra = total - per * blocks;
@@ -147,7 +199,7 @@ __device__ void sched_begin(const AttnParams& p, int min_units, Share* out, long
   const long long u1 = c < blocks ? u0 + per + (c < extra ? 1 : 0) : total;
   if (tid == 0) {
     out->u0 = u0; out->u1 = u1; out->total = total; out->per = per; out->extra = extra;
-    out->b = -1; out->h = out->mt = out->tile = 0;
+    out->b = -1; out->h = out->mt = out->off = 0;
   }
   __syncthreads();
   if (u0 < u1 && u0 >= ex && u0 < ex + mine) {
@@ -161,11 +213,11 @@ __device__ void sched_begin(const AttnParams& p, int min_units, Share* out, long
         rest -= h * hu;
         int mt = 0;
         for (;; ++mt) {
-          const int t = (S::klen(p, r, mt) + BK - 1) / BK;
+          const int t = S::item_units(p, r, mt);
           if (rest < t) break;
           rest -= t;
         }
-        out->b = b; out->h = h; out->mt = mt; out->tile = (int)rest;
+        out->b = b; out->h = h; out->mt = mt; out->off = (int)rest;
         break;
       }
       at += all;

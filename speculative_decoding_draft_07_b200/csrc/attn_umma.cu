@@ -15,7 +15,11 @@
 //     takes 1768 cycles for 128 tokens of a stream, two threads 1269;
 //   * warps 3-6 and 7-10: the softmax of stream 0 and 1. A thread reads its row of
 //     64 scores from tensor memory, keeps the running maximum and sum, and writes
-//     the weights back as bf16 over the scores.
+//     the weights back as bf16 over the scores. At an item's end they leave the
+//     rows in the item's query buffer;
+//   * warp 11: stores these rows by TMA (boxes like the queries'; rows past count
+//     are staged as zeros) and hands the buffer back to the producer. With the
+//     softmax warps storing them an item cost as much as 5.6 tiles.
 // With more than R rows in an item the streams are its two row tiles and share
 // every K and V tile; with fewer they take alternate key tiles of the same rows
 // and are added up at the item's end (both accumulators sit in the same tensor
@@ -40,7 +44,7 @@ namespace pct {
 namespace {
 
 constexpr int UBK = 64;                  // tokens of a key tile
-constexpr int UTHREADS = 352;
+constexpr int UTHREADS = 384;
 constexpr int UROWS = 256;               // row places of a piece (two streams of 128)
 constexpr int GONE = 8;                  // tiles whose bad-page marks are kept
 constexpr int ITEMS = 4;                 // published items
@@ -52,10 +56,7 @@ template <int DP> struct UShape {
   static constexpr int KHALF = UBK * 128;
   static constexpr int SLOT = HALVES * KHALF;
   static constexpr int SLOTS = DP == 128 ? 6 : 8;          // K and V tiles in flight
-  // exchange of the streams' (maximum, sum): behind the staged half rows of a
-  // query buffer, or (one box a row) behind the ring
-  static constexpr int EXTRA = HALVES == 2 ? 0 : 2 * 128 * 8;
-  static constexpr size_t SMEM = 1024 + 4 * QTILE + SLOTS * SLOT + EXTRA;
+  static constexpr size_t SMEM = 1024 + 4 * QTILE + SLOTS * SLOT;
 };
 
 struct UMaps {
@@ -70,6 +71,14 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int x, int y,
+                                             int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(z), "r"(w), "r"(src)
       : "memory");
 }
 // D += A B with A (bf16 pairs) in tensor memory
@@ -131,14 +140,15 @@ __device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
 template <int DP>
 __global__ void __launch_bounds__(UTHREADS, 1)
 attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                 const __grid_constant__ CUtensorMap tmV, const AttnParams p, const UMaps mp) {
+                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                 const AttnParams p, const UMaps mp) {
   typedef UShape<DP> U;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sQ = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));   // [stream][2]
   uint8_t* ring = sQ + 4 * U::QTILE;
   __shared__ uint64_t full[U::SLOTS], empty[U::SLOTS], qfull[2][2], qempty[2][2], sfull[2][2],
-      pready[2][2], pvdone[2][2], item_full[ITEMS], pair, group[2], drain[2];
+      pready[2][2], pvdone[2][2], staged[2][2], item_full[ITEMS], pair, drain[2];
   __shared__ Item items[ITEMS];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
@@ -154,18 +164,17 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     for (int i = 0; i < 2; ++i) {
       for (int j = 0; j < 2; ++j) {
         mbar_init(&qfull[i][j], 1);
-        mbar_init(&qempty[i][j], 128);
+        mbar_init(&qempty[i][j], 1);
+        mbar_init(&staged[i][j], 128);
         mbar_init(&sfull[i][j], 1);
         mbar_init(&pready[i][j], 128);
         mbar_init(&pvdone[i][j], 1);
       }
-      mbar_init(&group[i], 128);
       mbar_init(&drain[i], 1);
     }
     for (int i = 0; i < ITEMS; ++i) mbar_init(&item_full[i], 1);
     mbar_init(&pair, 256);
     abort_word = 0;
-    *err = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_async_smem();
   }
@@ -175,7 +184,10 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                  "r"(512));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  sched_begin<UBK, UTHREADS>(p, 1, &share, sums);
+  pdl_wait();      // the set-up above touches only shared memory and TMEM
+  pdl_trigger();
+  if (tid == 0) *err = 0;
+  sched_begin<UBK, UTHREADS>(p, &share, sums);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -183,31 +195,19 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
-    typedef Sched<UBK> S;
-    long long u = share.u0;
-    int b = share.b, h = share.h, mt = share.mt, t0 = share.tile, seq0 = 0, n_items = 0;
+    Walk<UBK> w;
+    w.begin(share);
+    int seq0 = 0, n_items = 0;
     int4 begun = make_int4(-1, 0, 0, 0);
-    Req r;
-    r.n = 0;
-    bool ok = true, fresh = true;
+    bool ok = true;
     uint32_t armed = 0;                              // ring slots used
     int slot = 0;
     uint32_t par = 0;
     const int boxes = UBK >> mp.shift;               // boxes of a tile
     const int nodes = mp.rows / p.g;                 // nodes of a row tile
     while (ok) {
-      const bool end = u >= share.u1;
-      int klen = 0, nt = 0, t1 = t0, rows = 0;
-      if (!end) {
-        if (fresh) r = attn_req(p, b);
-        fresh = false;
-        if (mt >= S::row_tiles(p, r)) { mt = 0; ++h; }
-        while (h >= p.hkv || r.n == 0) { ++b; h = 0; mt = 0; r = attn_req(p, b); }
-        klen = S::klen(p, r, mt);
-        nt = (klen + UBK - 1) / UBK;
-        t1 = (int)min((long long)nt, t0 + (share.u1 - u));
-        rows = min(p.bm, r.n * p.g - mt * p.bm);
-      }
+      const bool end = !w.next(p, share, &begun);
+      const int b = w.b, h = w.h, mt = w.mt - 1, t0 = w.t0, t1 = w.t1, klen = w.klen, rows = w.rows;
       const int buf = n_items & 1;
       const uint32_t qpar = (uint32_t)(n_items >> 1) & 1u;
 #pragma unroll
@@ -223,11 +223,9 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       if (lane == 0) {
         Item& it = items[n_items % ITEMS];
         it.b = b; it.h = h; it.mt = mt; it.t0 = t0; it.t1 = t1; it.rows = rows; it.klen = klen;
-        it.ctx = (int)r.ctx; it.seq = seq0; it.last = end; it.split = split;
-        it.whole = t0 == 0 && t1 == nt;
-        it.pslot = u == share.u0 ? 0 : 1;
-        if (!end && t0 == 0 && t1 < nt)
-          begun = make_int4(b, h, mt, it.pslot | block_of(share, u + nt - 1) << 1);
+        it.ctx = (int)w.r.ctx; it.seq = seq0; it.last = end; it.split = split;
+        it.whole = w.whole;
+        it.pslot = w.pslot;
         mbar_arrive(&item_full[n_items % ITEMS]);
         if (!end) {
 #pragma unroll
@@ -284,9 +282,6 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
       }
       seq0 += t1 - t0;
-      u += t1 - t0;
-      t0 = 0;
-      ++mt;
     }
     if (lane == 0) p.meta[blockIdx.x] = begun;
     // every copy has landed before the block may exit: slot i was last armed in the
@@ -391,6 +386,38 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       umma_commit(&drain[s]);
       drain_wait(&drain[s], 0);
     }
+  } else if (warp == 11) {
+    if (lane == 0) {
+      // ---------------- output rows ----------------
+      const int nodes = mp.rows / p.g;
+      for (int i = 0;; ++i) {
+        if (!wait_bar(&item_full[i % ITEMS], (uint32_t)(i / ITEMS) & 1u, abort_flag, err)) break;
+        const Item& w = items[i % ITEMS];
+        if (w.last) break;
+        const int buf = i & 1;
+        const uint32_t par = (uint32_t)(i >> 1) & 1u;
+        bool got = true;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          got = got && wait_bar(&staged[s][buf], par, abort_flag, err);
+          // both streams of a split item stage in stream 0's buffer
+          const int first = (w.mt * 2 + s) * nodes;
+          if (got && w.whole && (w.split ? s == 1 : first < p.n)) {
+            const uint32_t src = smem_u32(sQ + ((w.split ? 0 : s) * 2 + buf) * U::QTILE);
+#pragma unroll
+            for (int hf = 0; hf < U::HALVES; ++hf)
+              tma_store_4d(&tmO, src + hf * U::QHALF, hf * 64, w.h * p.g,
+                           w.split ? w.mt * 2 * nodes : first, w.b);
+          }
+        }
+        if (!got) break;
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        mbar_arrive(&qempty[0][buf]);
+        mbar_arrive(&qempty[1][buf]);
+      }
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
   } else {
     // ---------------- softmax ----------------
     const int s = (warp - 3) >> 2, quad = warp & 3;
@@ -400,7 +427,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const uint32_t aS = tS + s * 128 + lane_base, aO = tO + s * DP + lane_base;
     const float c = p.scale_log2;
     int n = 0, n_items = 0;                              // tiles of this stream, items
-    uint32_t met = 0, met_group = 0;
+    uint32_t met = 0;
     auto wait = [&](uint64_t* bar, uint32_t par) {
       const bool got = wait_bar(bar, par, abort_flag, err);
       return __all_sync(0xffffffffu, got);
@@ -408,10 +435,6 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     auto pair_sync = [&]() {                             // both softmax groups (bounded)
       mbar_arrive(&pair);
       (void)wait(&pair, met++ & 1u);
-    };
-    auto group_sync = [&]() {                            // this one
-      mbar_arrive(&group[s]);
-      (void)wait(&group[s], met_group++ & 1u);
     };
     for (;; ++n_items) {
       const int slot_i = n_items % ITEMS, buf = n_items & 1;
@@ -517,24 +540,25 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         (void)wait(&pvdone[s][(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u);
         tc_fence_after();
       }
-      // O to the caller, through this item's query buffer (its products are complete)
-      // so that rows go out in full lines; pieces directly, [d / 4][row][4]
-      uint8_t* stage = sQ + (s * 2 + buf) * U::QTILE;
+      // O to the caller, through this item's query buffer (its products are complete);
+      // pieces directly, [d / 4][row][4]
       const float ms = m == neg_inf() ? m : m * c;       // log2 units
       const long long piece = (long long)blockIdx.x * 2 + w.pslot;
       const int place = (split ? 0 : s * 128) + tl;
       float4* po = reinterpret_cast<float4*>(p.po) + piece * (p.d / 4) * UROWS + place;
-      auto put = [&](int col, const float (&y)[8], int chunk) {   // 8 columns from `col`
+      uint8_t* stage = sQ + ((split ? 0 : s) * 2 + buf) * U::QTILE + tl * 128;
+      auto put = [&](int col, const float (&y)[8]) {     // 8 columns from `col`
         if (whole) {
-          *reinterpret_cast<uint4*>(stage + (chunk >> 3) * U::QHALF + tl * 128 +
-                                    (((chunk & 7) ^ (tl & 7)) << 4)) = pack8(y);
+          const int ch = col / 8;
+          *reinterpret_cast<uint4*>(stage + (ch >> 3) * U::QHALF + (((ch & 7) ^ (tl & 7)) << 4)) =
+              valid ? pack8(y) : make_uint4(0, 0, 0, 0);
         } else if (valid && col < p.d) {
           po[(col / 4) * UROWS] = make_float4(y[0], y[1], y[2], y[3]);
           po[(col / 4 + 1) * UROWS] = make_float4(y[4], y[5], y[6], y[7]);
         }
       };
-      const int col0 = split ? s * (DP / 2) : 0, chunks = split ? DP / 16 : DP / 8;
-      (void)wait(&qfull[s][buf], (uint32_t)(n_items >> 1) & 1u);   // a stream without tiles
+      // (a stream without tiles has not seen its queries arrive)
+      (void)wait(&qfull[s][buf], (uint32_t)(n_items >> 1) & 1u);
       float row_m = ms, row_l = l;
       if (!split) {
         const float f = whole ? inverse(l) : 1.f;
@@ -549,20 +573,20 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             float y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(o[q * 8 + e]) * f;
-            put(j * 16 + q * 8, y, j * 2 + q);
+            put(j * 16 + q * 8, y);
           }
         }
       } else {
         // the two streams hold the same rows: each group adds up half of the columns
-        auto ml = [&](int st) {
-          return reinterpret_cast<float2*>(U::EXTRA ? ring + U::SLOTS * U::SLOT + st * 128 * 8
-                                                    : sQ + (st * 2 + buf) * U::QTILE + U::QHALF) + tl;
-        };
-        *ml(s) = make_float2(ms, l);
+        // (maxima and sums meet in stream 1's query buffer, free once both are here)
+        const int col0 = s * (DP / 2);
+        float2* ml = reinterpret_cast<float2*>(sQ + (2 + buf) * U::QTILE) + tl;
         tc_fence_before();
         pair_sync();
         tc_fence_after();
-        const float2 a = *ml(0), b = *ml(1);
+        ml[s * 128] = make_float2(ms, l);
+        pair_sync();
+        const float2 a = ml[0], b = ml[128];
         row_m = fmaxf(a.x, b.x);
         const float ref = row_m == neg_inf() ? 0.f : row_m;
         const float fa = ex2(a.x - ref), fb = ex2(b.x - ref);
@@ -587,7 +611,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               if (two) y[e] = fmaf(__uint_as_float(o2[q * 8 + e]), fb, y[e]);
               y[e] *= f;
             }
-            put(col0 + j * 16 + q * 8, y, j * 2 + q);
+            put(col0 + j * 16 + q * 8, y);
           }
         }
         tc_fence_before();
@@ -600,21 +624,9 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           p.lse[((long long)w.b * p.n + node) * p.hq + w.h * p.g + (row0 + tl - node * p.g)] =
               lse_of(row_m == neg_inf() ? 0.f : row_m, row_l);
       }
-      if (whole) {
-        group_sync();
-        const int ch = tl % chunks, col = col0 + ch * 8;
-        for (int rr = tl / chunks; rr < lim; rr += 128 / chunks) {
-          const int row = row0 + rr, nd = row / p.g;
-          const long long o = ((long long)w.b * p.n + nd) * p.hq + w.h * p.g + (row - nd * p.g);
-          const uint4 y = *reinterpret_cast<const uint4*>(stage + (ch >> 3) * U::QHALF + rr * 128 +
-                                                          (((ch & 7) ^ (rr & 7)) << 4));
-          if (col < p.d)
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + o * p.d + col) = y;
-        }
-      }
-      fence_async_smem();                                // the buffer's next writer is a copy
+      fence_async_smem();                                // the buffer's next user is a copy
       tc_fence_before();
-      mbar_arrive(&qempty[s][buf]);
+      mbar_arrive(&staged[s][buf]);
     }
   }
   tc_fence_before();
@@ -628,7 +640,8 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 }
 
 // Joins the pieces of the split item that block blockIdx.x began: a thread a row and
-// every fourth 4-column group, pieces in unit order.
+// two 4-column groups (blockIdx.y: 8 groups of 32 rows x 4 of columns, so that a few
+// split items still spread over the device), pieces in unit order, eight loads ahead.
 __global__ void __launch_bounds__(128) attn_umma_join_kernel(AttnParams p, int rows_tile) {
   pdl_wait();
   pdl_trigger();
@@ -640,20 +653,19 @@ __global__ void __launch_bounds__(128) attn_umma_join_kernel(AttnParams p, int r
   const int b = m.x, h = m.y, mt = m.z, slot = m.w & 1, last = m.w >> 1;
   const Req r = attn_req(p, b);
   const int rows = min(p.bm, r.n * p.g - mt * p.bm);
-  const int place = blockIdx.y * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+  const int place = (blockIdx.y >> 2) * 32 + (threadIdx.x & 31);
+  const int w = (blockIdx.y & 3) * 4 + (threadIdx.x >> 5);       // column groups w, w + 16
   const int s = place >> 7, rr = place & 127;
-  if (rr >= rows_tile || s * rows_tile + rr >= rows) return;
+  const int d4 = p.d / 4;
+  if (rr >= rows_tile || s * rows_tile + rr >= rows || w >= d4) return;
   auto ml = [&](int k) { return p.pml[((long long)k * 2 + (k == c ? slot : 0)) * UROWS + place]; };
   float mx = neg_inf();
-#pragma unroll 4
+#pragma unroll 8
   for (int k = c; k <= last; ++k) mx = fmaxf(mx, ml(k).x);
   const float ref = mx == neg_inf() ? 0.f : mx;
-  const int d4 = p.d / 4;
-  float4 acc[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
   float l = 0.f;
-#pragma unroll 2
+#pragma unroll 4
   for (int k = c; k <= last; ++k) {
     const float2 a = ml(k);
     const float f = ex2(a.x - ref);
@@ -661,9 +673,9 @@ __global__ void __launch_bounds__(128) attn_umma_join_kernel(AttnParams p, int r
     const float4* po = reinterpret_cast<const float4*>(p.po) +
                        ((long long)k * 2 + (k == c ? slot : 0)) * d4 * UROWS + place;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (w + 4 * j < d4) {
-        const float4 x = po[(w + 4 * j) * UROWS];
+    for (int j = 0; j < 2; ++j)
+      if (w + 16 * j < d4) {
+        const float4 x = po[(w + 16 * j) * UROWS];
         acc[j].x = fmaf(x.x, f, acc[j].x); acc[j].y = fmaf(x.y, f, acc[j].y);
         acc[j].z = fmaf(x.z, f, acc[j].z); acc[j].w = fmaf(x.w, f, acc[j].w);
       }
@@ -672,9 +684,9 @@ __global__ void __launch_bounds__(128) attn_umma_join_kernel(AttnParams p, int r
   const long long o = ((long long)b * p.n + node) * p.hq + h * p.g + (row - node * p.g);
   const float inv = inverse(l);
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (w + 4 * j < d4)
-      store_out(static_cast<__nv_bfloat16*>(p.out) + o * p.d + (w + 4 * j) * 4,
+  for (int j = 0; j < 2; ++j)
+    if (w + 16 * j < d4)
+      store_out(static_cast<__nv_bfloat16*>(p.out) + o * p.d + (w + 16 * j) * 4,
                 make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv));
   if (p.lse && w == 0) p.lse[o] = lse_of(ref, l);
 }
@@ -707,32 +719,34 @@ bool encode_cache(CUtensorMap* map, const void* base, const AttnParams& p, int r
   return encode_4d(map, base, dims, strides, box);
 }
 // [batch][n][heads][d], boxes of 64 columns x a group's heads x the nodes of a row tile
-bool encode_q(CUtensorMap* map, const AttnParams& p, int nodes) {
+bool encode_rows(CUtensorMap* map, const void* base, const AttnParams& p, int64_t s_b, int64_t s_n,
+                 int64_t s_h, int nodes) {
   const cuuint64_t row = (cuuint64_t)(p.d * 2 + 15) / 16 * 16;
-  const cuuint64_t head = p.hq > 1 ? (cuuint64_t)p.qs_h * 2 : row;
-  const cuuint64_t node = p.n > 1 ? (cuuint64_t)p.qs_n * 2 : head;
-  const cuuint64_t req = p.batch > 1 ? (cuuint64_t)p.qs_b * 2 : node;
+  const cuuint64_t head = p.hq > 1 ? (cuuint64_t)s_h * 2 : row;
+  const cuuint64_t node = p.n > 1 ? (cuuint64_t)s_n * 2 : head;
+  const cuuint64_t req = p.batch > 1 ? (cuuint64_t)s_b * 2 : node;
   const cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)p.hq, (cuuint64_t)p.n, (cuuint64_t)p.batch};
   const cuuint64_t strides[3] = {head, node, req};
   const cuuint32_t box[4] = {64, (cuuint32_t)p.g, (cuuint32_t)nodes, 1};
-  return encode_4d(map, p.q, dims, strides, box);
+  return encode_4d(map, base, dims, strides, box);
 }
 
 template <int DP>
 cudaError_t run_umma(const AttnParams& p, const CUtensorMap& q, const CUtensorMap& k,
-                     const CUtensorMap& v, const UMaps& mp, int grid, cudaStream_t s) {
+                     const CUtensorMap& v, const CUtensorMap& o, const UMaps& mp, int grid,
+                     cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(attn_umma_kernel<DP>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)UShape<DP>::SMEM);
   if (e != cudaSuccess) return e;
   {
     TraceScope t(s, "attn_umma");
-    attn_umma_kernel<DP><<<grid, UTHREADS, UShape<DP>::SMEM, s>>>(q, k, v, p, mp);
-    e = cudaGetLastError();
+    e = launch_pdl(attn_umma_kernel<DP>, dim3(grid), dim3(UTHREADS), UShape<DP>::SMEM, s, 1, q, k,
+                   v, o, p, mp);
   }
   if (e != cudaSuccess) return e;
   TraceScope t(s, "attn_umma_join");
-  return launch_pdl(attn_umma_join_kernel, dim3(grid, UROWS / 32), dim3(128), 0, s, 1, p, mp.rows);
+  return launch_pdl(attn_umma_join_kernel, dim3(grid, UROWS / 32 * 4), dim3(128), 0, s, 1, p, mp.rows);
 }
 
 }  // namespace
@@ -747,7 +761,7 @@ bool attn_umma_pages(int page_size) {
 
 // cudaErrorNotSupported when the strides do not fit a tensor map.
 cudaError_t launch_attn_umma(AttnParams p, int grid, cudaStream_t s) {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o;
   UMaps mp;
   const int rows = std::min(p.page_size, UBK);
   mp.shift = 0;
@@ -755,10 +769,18 @@ cudaError_t launch_attn_umma(AttnParams p, int grid, cudaStream_t s) {
   const int nodes = 128 / p.g;
   mp.rows = nodes * p.g;
   p.bm = 2 * mp.rows;
-  if (!encode_q(&q, p, nodes) || !encode_cache(&k, p.k, p, rows, &mp.slot_dim) ||
+  // costs fitted to the cycles of 148 blocks over mixed items
+  p.half = mp.rows;
+  p.many = 4;
+  p.few = 3;
+  p.per_item = 8;
+  const int64_t row = (int64_t)p.hq * p.d;
+  if (!encode_rows(&q, p.q, p, p.qs_b, p.qs_n, p.qs_h, nodes) ||
+      !encode_rows(&o, p.out, p, row * p.n, row, p.d, nodes) || !encode_cache(&k, p.k, p, rows, &mp.slot_dim) ||
       !encode_cache(&v, p.v, p, rows, &mp.slot_dim))
     return cudaErrorNotSupported;
-  return p.d <= 64 ? run_umma<64>(p, q, k, v, mp, grid, s) : run_umma<128>(p, q, k, v, mp, grid, s);
+  return p.d <= 64 ? run_umma<64>(p, q, k, v, o, mp, grid, s)
+                  : run_umma<128>(p, q, k, v, o, mp, grid, s);
 }
 
 }  // namespace pct

@@ -34,7 +34,6 @@ __device__ __forceinline__ float4 load4(const float* p) {
 template <int RPT, int DC>
 __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(AttnParams p) {
   constexpr int BM = 8 * RPT, BK = kSimtBK, NT = kSimtThreads;
-  typedef Sched<BK> S;
   extern __shared__ __align__(16) float sm[];
   __shared__ Share share;
   __shared__ long long sums[NT / 32];
@@ -45,19 +44,15 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(AttnParams p) {
   float* Vs = Ks + BK * dp;                // [BK][dp]
   float* Ps = Vs + BK * dp;                // [BK][BM]
   const int tid = threadIdx.x, rg = tid >> 4, cg = tid & 15;
-  sched_begin<BK, NT>(p, 2, &share, sums);
+  sched_begin<BK, NT>(p, &share, sums);
   int4 begun = make_int4(-1, 0, 0, 0);
 
-  long long u = share.u0;
-  int b = share.b, h = share.h, mt = share.mt, t0 = share.tile;
-  while (u < share.u1) {
-    Req r = attn_req(p, b);
-    const int nm = S::row_tiles(p, r);
-    if (mt >= nm) { mt = 0; ++h; }
-    while (h >= p.hkv || r.n == 0) { ++b; h = 0; mt = 0; r = attn_req(p, b); }
-    const int klen = S::klen(p, r, mt), nt = (klen + BK - 1) / BK;
-    const int t1 = (int)min((long long)nt, t0 + (share.u1 - u));
-    const int row0 = mt * BM, rows = min(BM, r.n * p.g - row0);
+  Walk<BK> w;
+  w.begin(share);
+  while (w.next(p, share, &begun)) {
+    const Req r = w.r;
+    const int b = w.b, h = w.h, t0 = w.t0, t1 = w.t1, klen = w.klen, rows = w.rows;
+    const int row0 = (w.mt - 1) * BM;
     const int32_t* table = p.table + (long long)b * p.max_pages;
 
     __syncthreads();
@@ -173,8 +168,8 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(AttnParams p) {
         }
       }
     }
-    const bool whole = t0 == 0 && t1 == nt;
-    const int slot = u == share.u0 ? 0 : 1;
+    const bool whole = w.whole;
+    const int slot = w.pslot;
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int rr = rg * RPT + i;
@@ -205,11 +200,6 @@ __global__ void __launch_bounds__(kSimtThreads) attn_simt_kernel(AttnParams p) {
         if (cg == 0) p.pml[at] = make_float2(m[i], l[i]);
       }
     }
-    if (t0 == 0 && t1 < nt)
-      begun = make_int4(b, h, mt, slot | block_of(share, u + nt - 1) << 1);
-    u += t1 - t0;
-    t0 = 0;
-    ++mt;
   }
   if (tid == 0) p.meta[blockIdx.x] = begun;
   attn_tail<float>(p);
@@ -301,7 +291,9 @@ cudaError_t launch_attn(const AttnArgs& a, void* ws, cudaStream_t s) {
   p.pml = reinterpret_cast<float2*>(w + P.o_ml);
   p.meta = reinterpret_cast<int4*>(w + P.o_meta);
   p.fail = nullptr;
-  p.bm = P.bm;
+  p.bm = p.half = P.bm;
+  p.few = p.many = 1;
+  p.per_item = 0;
   // the tcgen05 kernel scales masked (-inf) scores and takes maxima before scaling
   if (P.umma && a.scale > 0.f) {
     AttnParams up = p;
