@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -436,57 +437,100 @@ def cadd_cost_fit(n: torch.Tensor, ell: torch.Tensor, lat: torch.Tensor, stream=
 # ---------------------------------------------------------------------------
 # Paged key-value cache. Unlike the calls above, these take strided views where
 # the ABI does, make the tensors' device current for the call when it is not,
-# and allocate their outputs and workspace on the stream they run on.
+# and allocate their outputs and workspace on the stream they run on. Several run
+# once a layer or a round with little GPU work behind them, so the checks take one
+# fast look first, and what follows from shapes and strides alone (descriptors,
+# stride arrays, workspace sizes) is worked out once per combination.
 _HERE_ALREADY = contextlib.nullcontext()
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
 
 def _on(t: torch.Tensor, name: str, stream):
-    """(stream handle, context to allocate and launch in) for work on t's device."""
+    """(device, stream handle, context to allocate and launch in) for work on t's device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     dev = t.device
-    if dev.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} is on {dev}, expected a CUDA device")
     if stream is None:
-        s = torch.cuda.current_stream(dev)
-        if dev.index == torch.cuda.current_device():
-            return s.cuda_stream, _HERE_ALREADY
-    else:
-        s = stream
-        if s.device != dev:
-            raise ValueError(f"stream is on {s.device}, {name} on {dev}")
-    return s.cuda_stream, torch.cuda.stream(s)
+        if dev.index == torch._C._cuda_getDevice():
+            return dev, torch._C._cuda_getCurrentRawStream(dev.index), _HERE_ALREADY
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, {name} on {dev}")
+    return dev, stream.cuda_stream, torch.cuda.stream(stream)
 
 
-def _strides(t: torch.Tensor, name: str, dev, shape, dtype=None):
+def _want(t: torch.Tensor, name: str, dev: torch.device, shape, dtype):
+    """_check, with the common case first."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == dev and t.is_contiguous()):
+        _check(t, name, dev, shape, dtype)
+
+
+def _given(t: Optional[torch.Tensor], name: str, dev: torch.device, shape, dtype) -> torch.Tensor:
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _want(t, name, dev, shape, dtype)
+    return t
+
+
+def _rows(t: torch.Tensor, name: str, dev: torch.device, dtype):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-dimensional tensor")
+    if not (t.dtype is dtype and t.device == dev and t.is_contiguous()):
+        _check(t, name, dev, dtype=dtype)
+    return t.shape
+
+
+@functools.lru_cache(maxsize=1024)
+def _strides(shape, stride, name: str):
     """The element strides of all but the last axis of a view whose last axis is
-    contiguous (0 for an axis of one entry, which is never stepped over)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    st = t.stride()
-    if st[-1] != 1 and t.shape[-1] != 1:
+    contiguous (0 for an axis of one entry, which is never stepped over), as an array."""
+    if stride[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    return [0 if n == 1 else x for n, x in zip(t.shape[:-1], st[:-1])]
+    st = [0 if n == 1 else x for n, x in zip(shape[:-1], stride[:-1])]
+    return (ctypes.c_int64 * len(st))(*st)
 
 
-def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, max_pages: int, layered: bool = False):
-    """(descriptor, layer stride) of K and V caches [layers][n_pages][page_size][heads][head_dim]
-    (no layer axis unless `layered`)."""
+def _view(t: torch.Tensor, name: str, dev: torch.device, shape, dtype):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == dev):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    return _strides(t.shape, t.stride(), name)
+
+
+@functools.lru_cache(maxsize=1024)
+def _cache_desc(shape, stride, code: int, max_pages: int):
+    """(descriptor, a reference to it, layer stride) of a cache's shape and strides."""
+    st = list(_strides(shape, stride, "k_cache"))
+    d = KvCacheDesc(*shape[-4:-2], max_pages, *shape[-2:], code, *st[-3:])
+    return d, ctypes.byref(d), st[0] if len(shape) == 5 else 0
+
+
+def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, dev: torch.device, max_pages: int,
+           layered: bool = False):
+    """_cache_desc of K and V caches [layers][n_pages][page_size][heads][head_dim] (no layer
+    axis unless `layered`)."""
     dims = 5 if layered else 4
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != dims:
         raise ValueError("k_cache must be a %d-dimensional tensor" % dims)
-    st = _strides(k_cache, "k_cache", k_cache.device, k_cache.shape)
-    if _strides(v_cache, "v_cache", k_cache.device, k_cache.shape, k_cache.dtype) != st:
-        raise ValueError("k_cache and v_cache must have the same strides")
-    n_pages, page_size, heads, d = k_cache.shape[-4:]
-    return (KvCacheDesc(n_pages, page_size, max_pages, heads, d, _code(k_cache), *st[-3:]),
-            st[0] if layered else 0)
+    if k_cache.device != dev:
+        raise ValueError(f"k_cache is on {k_cache.device}, expected {dev}")
+    shape, stride = k_cache.shape, k_cache.stride()
+    if not (isinstance(v_cache, torch.Tensor) and v_cache.dtype is k_cache.dtype
+            and v_cache.device == dev and v_cache.shape == shape and v_cache.stride() == stride):
+        st = _view(v_cache, "v_cache", dev, shape, k_cache.dtype)
+        if list(st) != list(_strides(shape, stride, "k_cache")):
+            raise ValueError("k_cache and v_cache must have the same strides")
+    return _cache_desc(shape, stride, _code(k_cache), max_pages)
 
 
 def kv_pages_resize(ctx_len: torch.Tensor, block_table: torch.Tensor, held: torch.Tensor,
@@ -497,26 +541,24 @@ def kv_pages_resize(ctx_len: torch.Tensor, block_table: torch.Tensor, held: torc
     ceil((ctx_len + count) / page_size) pages a request, with pages from and back to
     free_pages[:free_count] (int32 [n_pages] and [1]); held [batch] int32 counts each
     request's pages. ctx_len [batch] int64, count [batch] int32. Returns status [batch]."""
-    s, ctx = _on(block_table, "block_table", stream)
-    dev = block_table.device
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [batch][max_pages]")
-    batch, max_pages = block_table.shape
-    _check(block_table, "block_table", dev, dtype=torch.int32)
-    _check(ctx_len, "ctx_len", dev, (batch,), torch.int64)
-    _check(held, "held", dev, (batch,), torch.int32)
-    _check(free_pages, "free_pages", dev, dtype=torch.int32)
-    _check(free_count, "free_count", dev, (1,), torch.int32)
+    dev, s, ctx = _on(block_table, "block_table", stream)
+    batch, max_pages = _rows(block_table, "block_table", dev, _I32)
+    _want(ctx_len, "ctx_len", dev, (batch,), _I64)
+    _want(held, "held", dev, (batch,), _I32)
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError("free_pages must be a 1-dimensional tensor")
+    _want(free_pages, "free_pages", dev, free_pages.shape, _I32)
+    _want(free_count, "free_count", dev, (1,), _I32)
     if count is not None:
-        _check(count, "count", dev, (batch,), torch.int32)
+        _want(count, "count", dev, (batch,), _I32)
     with ctx:
-        if status is None:
-            status = torch.empty(batch, dtype=torch.int32, device=dev)
-        else:
-            _check(status, "status", dev, (batch,), torch.int32)
-        code = lib().kv_pages_resize(batch, page_size, max_pages, free_pages.numel(), _p(ctx_len),
-                                     _p(count), _p(block_table), _p(held), _p(free_pages),
-                                     _p(free_count), _p(status), s)
+        status = _given(status, "status", dev, (batch,), _I32)
+        code = lib().kv_pages_resize(batch, page_size, max_pages, free_pages.shape[0],
+                                     ctx_len.data_ptr(),
+                                     None if count is None else count.data_ptr(),
+                                     block_table.data_ptr(), held.data_ptr(),
+                                     free_pages.data_ptr(), free_count.data_ptr(),
+                                     status.data_ptr(), s)
     _raise(code, "kv_pages_resize")
     return status
 
@@ -529,32 +571,21 @@ def kv_tree_slots(ctx_len: torch.Tensor, count: torch.Tensor, block_table: torch
     """(slot, pos, status): cache slots and positions [batch][n_stride] int64 of the
     count[b] tokens after ctx_len[b]; depth [batch][n_stride] int32 (a tree's node
     depths) makes siblings share a position, None is a chain."""
-    s, ctx = _on(block_table, "block_table", stream)
-    dev = block_table.device
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [batch][max_pages]")
-    batch, max_pages = block_table.shape
-    _check(block_table, "block_table", dev, dtype=torch.int32)
-    _check(ctx_len, "ctx_len", dev, (batch,), torch.int64)
-    _check(count, "count", dev, (batch,), torch.int32)
+    dev, s, ctx = _on(block_table, "block_table", stream)
+    batch, max_pages = _rows(block_table, "block_table", dev, _I32)
+    _want(ctx_len, "ctx_len", dev, (batch,), _I64)
+    _want(count, "count", dev, (batch,), _I32)
     if depth is not None:
-        _check(depth, "depth", dev, (batch, n_stride), torch.int32)
+        _want(depth, "depth", dev, (batch, n_stride), _I32)
     with ctx:
-        if slot is None:
-            slot = torch.empty((batch, n_stride), dtype=torch.int64, device=dev)
-        else:
-            _check(slot, "slot", dev, (batch, n_stride), torch.int64)
-        if pos is None:
-            pos = torch.empty((batch, n_stride), dtype=torch.int64, device=dev)
-        else:
-            _check(pos, "pos", dev, (batch, n_stride), torch.int64)
-        if status is None:
-            status = torch.empty(batch, dtype=torch.int32, device=dev)
-        else:
-            _check(status, "status", dev, (batch,), torch.int32)
-        code = lib().kv_tree_slots(batch, n_stride, page_size, max_pages, n_pages, _p(ctx_len),
-                                   _p(count), _p(depth), _p(block_table), _p(slot), _p(pos),
-                                   _p(status), s)
+        slot = _given(slot, "slot", dev, (batch, n_stride), _I64)
+        pos = _given(pos, "pos", dev, (batch, n_stride), _I64)
+        status = _given(status, "status", dev, (batch,), _I32)
+        code = lib().kv_tree_slots(batch, n_stride, page_size, max_pages, n_pages,
+                                   ctx_len.data_ptr(), count.data_ptr(),
+                                   None if depth is None else depth.data_ptr(),
+                                   block_table.data_ptr(), slot.data_ptr(), pos.data_ptr(),
+                                   status.data_ptr(), s)
     _raise(code, "kv_tree_slots")
     return slot, pos, status
 
@@ -565,25 +596,19 @@ def kv_append(k_new: torch.Tensor, v_new: torch.Tensor, slot: torch.Tensor, k_ca
     """Rows k_new, v_new [batch][n_stride][heads][head_dim] (views with a contiguous
     last axis and equal strides) into the caches [n_pages][page_size][heads][head_dim] at
     slot [batch][n_stride] int64 (negative: skipped). Returns status [batch]."""
-    s, ctx = _on(k_cache, "k_cache", stream)
-    dev = k_cache.device
-    desc, _ = _cache(k_cache, v_cache, 1)
-    if not isinstance(slot, torch.Tensor) or slot.dim() != 2:
-        raise ValueError("slot must be [batch][n_stride]")
-    batch, n = slot.shape
-    _check(slot, "slot", dev, dtype=torch.int64)
+    dev, s, ctx = _on(k_cache, "k_cache", stream)
+    desc, ref, _ = _cache(k_cache, v_cache, dev, 1)
+    batch, n = _rows(slot, "slot", dev, _I64)
     shape = (batch, n, desc.heads_kv, desc.head_dim)
-    st = _strides(k_new, "k_new", dev, shape, k_cache.dtype)
-    if _strides(v_new, "v_new", dev, shape, k_cache.dtype) != st:
+    st = _view(k_new, "k_new", dev, shape, k_cache.dtype)
+    st_v = _view(v_new, "v_new", dev, shape, k_cache.dtype)
+    if st_v is not st and list(st_v) != list(st):
         raise ValueError("k_new and v_new must have the same strides")
     with ctx:
-        if status is None:
-            status = torch.empty(batch, dtype=torch.int32, device=dev)
-        else:
-            _check(status, "status", dev, (batch,), torch.int32)
-        code = lib().kv_append(ctypes.byref(desc), batch, n, _p(k_new), _p(v_new),
-                               (ctypes.c_int64 * 3)(*st), _p(slot), _p(k_cache), _p(v_cache),
-                               _p(status), s)
+        status = _given(status, "status", dev, (batch,), _I32)
+        code = lib().kv_append(ref, batch, n, k_new.data_ptr(), v_new.data_ptr(), st,
+                               slot.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                               status.data_ptr(), s)
     _raise(code, "kv_append")
     return status
 
@@ -595,11 +620,19 @@ class AttnOut:
     status: torch.Tensor
 
 
+@functools.lru_cache(maxsize=1024)
+def _attn_workspace(shape, stride, code: int, max_pages: int, batch: int, n_stride: int,
+                    heads_q: int, device: int) -> int:
+    return int(lib().tree_attention_workspace(_cache_desc(shape, stride, code, max_pages)[1], batch,
+                                              n_stride, heads_q))
+
+
 def tree_attention_workspace(k_cache: torch.Tensor, v_cache: torch.Tensor, max_pages: int,
                              batch: int, n_stride: int, heads_q: int) -> int:
     """Workspace bytes tree_attention needs for these shapes on the current device."""
-    desc, _ = _cache(k_cache, v_cache, max_pages)
-    return int(lib().tree_attention_workspace(ctypes.byref(desc), batch, n_stride, heads_q))
+    _cache(k_cache, v_cache, k_cache.device, max_pages)
+    return _attn_workspace(k_cache.shape, k_cache.stride(), _code(k_cache), max_pages, batch,
+                           n_stride, heads_q, torch.cuda.current_device())
 
 
 def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -613,44 +646,43 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     ctx_len [batch] int64, count [batch] int32 (None: n_stride for all), mask the words of
     tree_ancestor_mask [batch][n_stride][ceil(n_stride / 32)] int32 (None: a causal chain; a
     decode step with n_stride = 1). scale defaults to head_dim ** -0.5. Rows at or past count
-    are 0, their lse -inf."""
-    s, ctx = _on(q, "q", stream)
-    dev = q.device
+    are 0, their lse -inf. With out given, out.lse may be None."""
+    dev, s, ctx = _on(q, "q", stream)
     if q.dim() != 4:
         raise ValueError("q must be [batch][n_stride][heads_q][head_dim]")
     batch, n, hq, d = q.shape
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise ValueError("block_table must be [batch][max_pages]")
-    max_pages = block_table.shape[1]
-    _check(block_table, "block_table", dev, (batch, max_pages), torch.int32)
-    desc, _ = _cache(k_cache, v_cache, max_pages)
-    if k_cache.device != dev:
-        raise ValueError(f"k_cache is on {k_cache.device}, expected {dev}")
-    st = _strides(q, "q", dev, (batch, n, hq, desc.head_dim), k_cache.dtype)
-    _check(ctx_len, "ctx_len", dev, (batch,), torch.int64)
+    rows, max_pages = _rows(block_table, "block_table", dev, _I32)
+    if rows != batch:
+        raise ValueError(f"block_table has {rows} rows, expected {batch}")
+    desc, ref, _ = _cache(k_cache, v_cache, dev, max_pages)
+    st = _view(q, "q", dev, (batch, n, hq, desc.head_dim), k_cache.dtype)
+    _want(ctx_len, "ctx_len", dev, (batch,), _I64)
     if count is not None:
-        _check(count, "count", dev, (batch,), torch.int32)
+        _want(count, "count", dev, (batch,), _I32)
     if mask is not None:
-        _check(mask, "mask", dev, (batch, n, (n + 31) // 32), torch.int32)
+        _want(mask, "mask", dev, (batch, n, (n + 31) // 32), _I32)
     with ctx:
         if out is None:
             out = AttnOut(torch.empty((batch, n, hq, d), dtype=q.dtype, device=dev),
-                          torch.empty((batch, n, hq), dtype=torch.float32, device=dev),
-                          torch.empty(batch, dtype=torch.int32, device=dev))
+                          torch.empty((batch, n, hq), dtype=_F32, device=dev),
+                          torch.empty((batch,), dtype=_I32, device=dev))
         else:
-            _check(out.out, "out.out", dev, (batch, n, hq, d), q.dtype)
+            _want(out.out, "out.out", dev, (batch, n, hq, d), q.dtype)
             if out.lse is not None:
-                _check(out.lse, "out.lse", dev, (batch, n, hq), torch.float32)
-            _check(out.status, "out.status", dev, (batch,), torch.int32)
-        nbytes = int(lib().tree_attention_workspace(ctypes.byref(desc), batch, n, hq))
+                _want(out.lse, "out.lse", dev, (batch, n, hq), _F32)
+            _want(out.status, "out.status", dev, (batch,), _I32)
+        nbytes = _attn_workspace(k_cache.shape, k_cache.stride(), desc.dtype, max_pages, batch, n,
+                                 hq, dev.index)
         if nbytes == 0:
             _raise(PCT_EINVAL, "tree_attention_workspace")
         ws, wsb = _workspace(nbytes, dev, workspace)
-        code = lib().tree_attention(ctypes.byref(desc), batch, n, hq,
-                                    d ** -0.5 if scale is None else scale, _p(q),
-                                    (ctypes.c_int64 * 3)(*st), _p(k_cache), _p(v_cache),
-                                    _p(block_table), _p(ctx_len), _p(count), _p(mask), _p(out.out),
-                                    _p(out.lse), _p(out.status), _p(ws), wsb, s)
+        code = lib().tree_attention(ref, batch, n, hq, d ** -0.5 if scale is None else scale,
+                                    q.data_ptr(), st, k_cache.data_ptr(), v_cache.data_ptr(),
+                                    block_table.data_ptr(), ctx_len.data_ptr(),
+                                    None if count is None else count.data_ptr(),
+                                    None if mask is None else mask.data_ptr(), out.out.data_ptr(),
+                                    None if out.lse is None else out.lse.data_ptr(),
+                                    out.status.data_ptr(), ws.data_ptr(), wsb, s)
     _raise(code, "tree_attention")
     return out
 
@@ -663,35 +695,26 @@ def kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.T
     accept_path [batch][max_depth] int32, as tree_verify_accept writes them) move behind the
     root in every layer of the caches [layers][n_pages][page_size][heads][head_dim] (or one
     layer without that axis), in place; new_len = ctx_len + 1 + accept_len."""
-    s, ctx = _on(k_cache, "k_cache", stream)
-    dev = k_cache.device
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise ValueError("block_table must be [batch][max_pages]")
-    batch, max_pages = block_table.shape
-    _check(block_table, "block_table", dev, dtype=torch.int32)
+    dev, s, ctx = _on(k_cache, "k_cache", stream)
+    batch, max_pages = _rows(block_table, "block_table", dev, _I32)
     layered = k_cache.dim() == 5
-    desc, layer_stride = _cache(k_cache, v_cache, max_pages, layered)
-    _check(ctx_len, "ctx_len", dev, (batch,), torch.int64)
-    _check(count, "count", dev, (batch,), torch.int32)
-    _check(accept_len, "accept_len", dev, (batch,), torch.int32)
-    if not isinstance(accept_path, torch.Tensor) or accept_path.dim() != 2:
-        raise ValueError("accept_path must be [batch][max_depth]")
-    _check(accept_path, "accept_path", dev, (batch, accept_path.shape[1]), torch.int32)
+    _, ref, layer_stride = _cache(k_cache, v_cache, dev, max_pages, layered)
+    _want(ctx_len, "ctx_len", dev, (batch,), _I64)
+    _want(count, "count", dev, (batch,), _I32)
+    _want(accept_len, "accept_len", dev, (batch,), _I32)
+    rows, max_depth = _rows(accept_path, "accept_path", dev, _I32)
+    if rows != batch:
+        raise ValueError(f"accept_path has {rows} rows, expected {batch}")
     with ctx:
-        if new_len is None:
-            new_len = torch.empty(batch, dtype=torch.int64, device=dev)
-        else:
-            _check(new_len, "new_len", dev, (batch,), torch.int64)
-            if new_len.data_ptr() == ctx_len.data_ptr():
-                raise ValueError("new_len must not be ctx_len")
-        if status is None:
-            status = torch.empty(batch, dtype=torch.int32, device=dev)
-        else:
-            _check(status, "status", dev, (batch,), torch.int32)
-        code = lib().kv_commit(ctypes.byref(desc), batch, k_cache.shape[0] if layered else 1,
-                               layer_stride, accept_path.shape[1], _p(k_cache), _p(v_cache),
-                               _p(block_table), _p(ctx_len), _p(count), _p(accept_len),
-                               _p(accept_path), _p(new_len), _p(status), s)
+        new_len = _given(new_len, "new_len", dev, (batch,), _I64)
+        if new_len.data_ptr() == ctx_len.data_ptr():
+            raise ValueError("new_len must not be ctx_len")
+        status = _given(status, "status", dev, (batch,), _I32)
+        code = lib().kv_commit(ref, batch, k_cache.shape[0] if layered else 1, layer_stride,
+                               max_depth, k_cache.data_ptr(), v_cache.data_ptr(),
+                               block_table.data_ptr(), ctx_len.data_ptr(), count.data_ptr(),
+                               accept_len.data_ptr(), accept_path.data_ptr(), new_len.data_ptr(),
+                               status.data_ptr(), s)
     _raise(code, "kv_commit")
     return new_len, status
 
