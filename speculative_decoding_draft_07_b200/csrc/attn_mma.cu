@@ -50,7 +50,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 template <int DP> struct MmaShape {
-  static constexpr int STAGES = DP == 256 ? 2 : 3;
+  static constexpr int STAGES = 3;
   static constexpr int TILE = kMmaBK * DP * 2;         // bytes of a K (or V) tile
   static constexpr int MINB = DP == 256 ? 1 : 2;
 };
@@ -66,13 +66,17 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<DP>::MINB) attn_mma_kern
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Share share;
   __shared__ long long sums[NT / 32];
-  __shared__ unsigned long long gone[STAGES];          // keys of the tile whose page is bad
+  // per tile (ring of four): where its tokens' rows lie, -1 for none, and the keys
+  // whose page is bad. Worked out a tile ahead of the copies, one thread a token, so
+  // that no copy waits for the block table.
+  __shared__ long long where[4][BK];
+  __shared__ unsigned long long gone[4];
   __shared__ float2 ml[WK][BM];
   unsigned char* Qs = smem;                            // [BM][DP]
   unsigned char* ring = smem + BM * DP * 2;            // [STAGES][K, V][BK][DP]
   float* obuf = reinterpret_cast<float*>(ring);        // [WK][BM][DP + 8] at an item's end
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wm = warp % WM, wk = warp / WM;
-  if (tid < STAGES) gone[tid] = 0;
+  if (tid < 4) gone[tid] = 0;
   sched_begin<BK, NT>(p, &share, sums);
   int4 begun = make_int4(-1, 0, 0, 0);
 
@@ -87,36 +91,43 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<DP>::MINB) attn_mma_kern
     const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(p.k) + h * p.ks_head;
     const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(p.v) + h * p.ks_head;
 
+    auto find_tile = [&](int t) {
+      if (tid >= BK) return;
+      const int tok = t * BK + tid;
+      long long off = -1;
+      if (tok < klen) {
+        const uint32_t col = page_of(p, tok);
+        const int page = __ldg(table + col);
+        if (page >= 0 && page < p.n_pages)
+          off = page * p.ks_page + (tok - (int)col * p.page_size) * p.ks_slot;
+        else
+          atomicOr(&gone[t & 3], 1ull << tid);
+      }
+      where[t & 3][tid] = off;
+    };
     auto load_tile = [&](int t) {
       const int st = (t - t0) % STAGES;
-      const uint32_t kd = sm_addr(ring + st * 2 * TILE), vd = kd + TILE;
       constexpr int RS = NT / CH;                      // rows a pass
-      const int c = tid % CH;
+      const int c = tid % CH, r0 = tid / CH;
       const bool in = c * 8 < p.d;
+      const uint32_t kd = sm_addr(ring + st * 2 * TILE), vd = kd + TILE;
 #pragma unroll
       for (int i = 0; i < BK / RS; ++i) {
-        const int rr = i * RS + tid / CH, tok = t * BK + rr;
+        const int rr = i * RS + r0;
         const uint32_t at = rr * (DP * 2) + ((c ^ (rr & 7)) << 4);
-        long long off = 0;
-        int bytes = 0;
-        if (tok < klen) {
-          const uint32_t col = page_of(p, tok);
-          const int page = __ldg(table + col);
-          if (page >= 0 && page < p.n_pages) {
-            if (in) {
-              off = page * p.ks_page + (tok - (int)col * p.page_size) * p.ks_slot + c * 8;
-              bytes = 16;
-            }
-          } else {
-            atomicOr(&gone[st], 1ull << rr);
-          }
-        }
-        cp16(kd + at, kb + off, bytes);
-        cp16(vd + at, vb + off, bytes);
+        const long long w = where[t & 3][rr];
+        const bool on = in && w >= 0;
+        const long long off = on ? w + c * 8 : 0;
+        cp16(kd + at, kb + off, on ? 16 : 0);
+        cp16(vd + at, vb + off, on ? 16 : 0);
       }
     };
 
     __syncthreads();                                   // the last item's buffers are free
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i)
+      if (t0 + i < t1) find_tile(t0 + i);
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < BM * CH / NT; ++i) {
       const int rr = (i * NT + tid) / CH, c = tid % CH;
@@ -159,6 +170,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<DP>::MINB) attn_mma_kern
       __syncthreads();
       if (t + STAGES - 1 < t1) load_tile(t + STAGES - 1);
       cp_commit();
+      if (t + STAGES < t1) find_tile(t + STAGES);
       if (QREG && t == t0) {
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) ldsm4(qa + (((2 * k + (lane >> 4)) ^ (lane & 7)) << 4), qf[QREG ? k : 0]);
@@ -193,7 +205,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<DP>::MINB) attn_mma_kern
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[i][j] *= p.scale_log2;
       const int key0 = t * BK + wk * KW;               // the warp's first token
-      const unsigned long long lost = gone[st];
+      const unsigned long long lost = gone[t & 3];
       if (key0 + KW > ctx || lost) {                   // nodes, the end, or a bad page
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -260,7 +272,7 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<DP>::MINB) attn_mma_kern
       }
       if (lost) {                                      // rare: clear the mark for the stage's next tile
         __syncthreads();
-        if (tid == 0) gone[st] = 0;
+        if (tid == 0) gone[t & 3] = 0;
       }
     }
     cp_wait<0>();

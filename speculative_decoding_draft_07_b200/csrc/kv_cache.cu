@@ -221,47 +221,59 @@ struct RowGeom {
   int page_size;
 };
 
-// The rows' 16-byte pieces in order (request, token, K or V, head, piece), four
-// pieces a thread and pass, loads before stores.
+// A block moves kAppendRows tokens: one thread a token works out where its row comes
+// from and goes to, then the block copies 16-byte pieces, a thread one column (K or V,
+// head, piece) of several tokens, eight loads before their stores. No division runs
+// per piece (with two of 64 bits each, 32 x 1000 tokens of 8 x 128 bf16 took 63 us).
+constexpr int kAppendRows = 32;
+constexpr int kAppendLoads = 8;
 __global__ void __launch_bounds__(256)
-kv_append_kernel(RowGeom g, int batch, int n_stride, long long n_slots,
+kv_append_kernel(RowGeom g, int batch, int n_stride, long long n_slots, int cols,
                  const uint4* __restrict__ k_new, const uint4* __restrict__ v_new, long long s_b,
                  long long s_n, long long s_h, const int64_t* __restrict__ slot, uint4* k_cache,
                  uint4* v_cache, int32_t* status) {
-  const int row = g.heads * g.vec;
-  const long long rows = (long long)batch * n_stride, total = rows * 2 * row;
-  const long long step = (long long)gridDim.x * blockDim.x;
-  for (long long p0 = (long long)blockIdx.x * blockDim.x + threadIdx.x; p0 < total;
-       p0 += 4 * step) {
-    uint4 x[4];
-    uint4* to[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const long long p = p0 + j * step;
-      to[j] = nullptr;
-      if (p >= total) continue;
-      const long long r = p / (2 * row);
-      int c = (int)(p - r * (2 * row));
-      const bool is_v = c >= row;
-      if (is_v) c -= row;
-      const long long s = slot[r];
-      if (s < 0 || s >= n_slots) continue;
-      const int b = (int)(r / n_stride), i = (int)(r - (long long)b * n_stride);
-      const int h = c / g.vec, w = c - h * g.vec;
-      const long long pg = s / g.page_size, in = s - pg * g.page_size;
-      x[j] = ld_stream16((is_v ? v_new : k_new) + b * s_b + i * s_n + h * s_h + w);
-      to[j] = (is_v ? v_cache : k_cache) + pg * g.page + in * g.slot + h * g.head + w;
+  __shared__ long long from[kAppendRows], to[kAppendRows];
+  const int tid = threadIdx.x;
+  const long long rows = (long long)batch * n_stride, r0 = (long long)blockIdx.x * kAppendRows;
+  if (tid < kAppendRows) {
+    long long f = 0, t = -1;
+    if (r0 + tid < rows) {
+      const long long r = r0 + tid, s = slot[r];
+      if (s >= 0 && s < n_slots) {
+        const long long b = r / n_stride, pg = s / g.page_size;
+        f = b * s_b + (r - b * n_stride) * s_n;
+        t = pg * g.page + (s - pg * g.page_size) * g.slot;
+      }
     }
+    from[tid] = f;
+    to[tid] = t;
+  }
+  __syncthreads();
+  const int row = g.heads * g.vec, lanes = blockDim.x / cols, r1 = tid / cols;
+  if (r1 < lanes) {
+    for (int c = tid - r1 * cols; c < 2 * row; c += cols) {
+      const bool is_v = c >= row;
+      const int q = is_v ? c - row : c, h = q / g.vec, w = q - h * g.vec;
+      const uint4* src = (is_v ? v_new : k_new) + h * s_h + w;
+      uint4* dst = (is_v ? v_cache : k_cache) + h * g.head + w;
+      for (int r = r1; r < kAppendRows; r += kAppendLoads * lanes) {
+        uint4 x[kAppendLoads];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (to[j]) *to[j] = x[j];
+        for (int j = 0; j < kAppendLoads; ++j)
+          if (r + j * lanes < kAppendRows && to[r + j * lanes] >= 0)
+            x[j] = ld_stream16(src + from[r + j * lanes]);
+#pragma unroll
+        for (int j = 0; j < kAppendLoads; ++j)
+          if (r + j * lanes < kAppendRows && to[r + j * lanes] >= 0) dst[to[r + j * lanes]] = x[j];
+      }
+    }
   }
   for (int b = blockIdx.x; b < batch; b += gridDim.x) {
     int bad = 0;
-    for (int i = threadIdx.x; i < n_stride; i += blockDim.x)
+    for (int i = tid; i < n_stride; i += blockDim.x)
       bad |= slot[(long long)b * n_stride + i] >= n_slots;
     bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) status[b] = bad ? PCT_DEV_BAD_PAGE : 0;
+    if (tid == 0) status[b] = bad ? PCT_DEV_BAD_PAGE : 0;
   }
 }
 
@@ -382,14 +394,13 @@ cudaError_t launch_kv_append(const kv_cache_desc& d, int batch, int n_stride, co
   TraceScope t(s, "kv_append");
   const RowGeom g = geom(d);
   const int per = d.dtype == PCT_BF16 ? 8 : 4;
-  const long long total = (long long)batch * n_stride * 2 * g.heads * g.vec;
-  const long long blocks = (total + 1023) / 1024;
-  const int grid = (int)(blocks < 1 ? 1 : blocks > 148 * 64 ? 148 * 64 : blocks);
-  kv_append_kernel<<<grid, 256, 0, s>>>(
-      g, batch, n_stride, (long long)d.n_pages * d.page_size, static_cast<const uint4*>(k_new),
-      static_cast<const uint4*>(v_new), new_stride[0] / per, new_stride[1] / per,
-      new_stride[2] / per, slot, static_cast<uint4*>(k_cache), static_cast<uint4*>(v_cache),
-      status);
+  const int cols = g.heads * g.vec * 2 < 256 ? g.heads * g.vec * 2 : 256;   // columns a pass
+  const long long grid = ((long long)batch * n_stride + kAppendRows - 1) / kAppendRows;
+  kv_append_kernel<<<(unsigned)grid, 256, 0, s>>>(
+      g, batch, n_stride, (long long)d.n_pages * d.page_size, cols,
+      static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), new_stride[0] / per,
+      new_stride[1] / per, new_stride[2] / per, slot, static_cast<uint4*>(k_cache),
+      static_cast<uint4*>(v_cache), status);
   return cudaGetLastError();
 }
 
