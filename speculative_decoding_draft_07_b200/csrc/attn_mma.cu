@@ -77,6 +77,8 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<DP>::MINB) attn_mma_kern
   float* obuf = reinterpret_cast<float*>(ring);        // [WK][BM][DP + 8] at an item's end
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wm = warp % WM, wk = warp / WM;
   if (tid < 4) gone[tid] = 0;
+  pdl_wait();
+  pdl_trigger();
   sched_begin<BK, NT>(p, &share, sums);
   int4 begun = make_int4(-1, 0, 0, 0);
 
@@ -341,12 +343,11 @@ cudaError_t run_mma(const AttnParams& p, int grid, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   {
     TraceScope t(s, "attn_mma");
-    attn_mma_kernel<DP, WM><<<grid, kMmaThreads, smem, s>>>(p);
-    e = cudaGetLastError();
+    e = launch_pdl(attn_mma_kernel<DP, WM>, dim3(grid), dim3(kMmaThreads), smem, s, 1, p);
   }
   if (e != cudaSuccess) return e;
   TraceScope t(s, "attn_join");
-  return launch_pdl(attn_join_kernel<__nv_bfloat16, BM>, dim3(grid, (BM + 7) / 8), dim3(128), 0, s,
+  return launch_pdl(attn_join_kernel<__nv_bfloat16, BM, DP == 256>, dim3(grid, (BM + 3) / 4), dim3(128), 0, s,
                     1, p);
 }
 template <int DP>

@@ -37,7 +37,7 @@ struct AttnParams {
   int few, many, per_item;      // rows, `many` of one with more, `per_item` an item
   uint32_t pg_mul, pg_shift;    // t / page_size = (umulhi(t, mul) + t) >> shift
   int4* meta;                   // [grid] split item begun by the block: b (-1 none),
-                                // h, mt, slot | last block << 1
+                                // h | rows << 10, mt, slot | last block << 1
 };
 
 namespace {
@@ -152,7 +152,8 @@ struct Walk {
       whole = t0 == 0 && t1 == nt;
       pslot = u == s.u0 ? 0 : 1;
       if (t0 == 0 && t1 > 0 && t1 < nt)
-        *begun = make_int4(b, h, mt, pslot | block_of(s, u - off + c + (long long)(nt - 1) * w) << 1);
+        *begun = make_int4(b, h | rows << 10, mt,
+                           pslot | block_of(s, u - off + c + (long long)(nt - 1) * w) << 1);
       u += e - off;
       off = 0;
       ++mt;                      // (b, h, mt - 1) is the item in hand
@@ -271,53 +272,76 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* p, float4 v) {
   *reinterpret_cast<uint2*>(p) = w;
 }
 
+// A row's pieces, in unit order, with the running maximum. JOIN_AHEAD pieces' maxima,
+// sums and values are asked for together (unconditionally: past the last piece the
+// last one again, without weight), so the join waits for memory a few times and not
+// twice a piece.
+constexpr int JOIN_AHEAD = 8;
+struct JoinState {
+  float m, l;
+  __device__ __forceinline__ void begin() { m = neg_inf(); l = 0.f; }
+  // the factors of the sums so far and of the new piece
+  __device__ __forceinline__ float2 add(float2 a) {
+    const float mn = fmaxf(m, a.x), ref = mn == neg_inf() ? 0.f : mn;
+    const float2 f = make_float2(ex2(m - ref), ex2(a.x - ref));
+    l = l * f.x + a.y * f.y;
+    m = mn;
+    return f;
+  }
+};
+__device__ __forceinline__ void join_add(float4& acc, float4 x, float2 f) {
+  acc.x = fmaf(x.x, f.y, acc.x * f.x);
+  acc.y = fmaf(x.y, f.y, acc.y * f.x);
+  acc.z = fmaf(x.z, f.y, acc.z * f.x);
+  acc.w = fmaf(x.w, f.y, acc.w * f.x);
+}
+
 // Joins the pieces of the split item that block blockIdx.x of the attention
-// kernel began: one warp a row, its lanes over head_dim, pieces in unit order.
-template <typename T, int BM>
+// kernel began: one warp a row, its lanes over head_dim.
+template <typename T, int BM, bool WIDE>   // WIDE: head_dim above 128
 __global__ void __launch_bounds__(128) attn_join_kernel(AttnParams p) {
   pdl_wait();
   pdl_trigger();
   const int c = blockIdx.x;
   const int4 m = p.meta[c];
   if (m.x < 0) return;
-  const int b = m.x, h = m.y, mt = m.z, slot = m.w & 1, last = m.w >> 1;
-  const Req r = attn_req(p, b);
-  const int rows = min(BM, r.n * p.g - mt * BM);
+  const int b = m.x, h = m.y & 1023, rows = m.y >> 10, mt = m.z, slot = m.w & 1, last = m.w >> 1;
   const int lane = threadIdx.x & 31;
+  const int d0 = lane * 4 < p.d ? lane * 4 : 0, d1 = lane * 4 + 128 < p.d ? lane * 4 + 128 : 0;
   for (int i = blockIdx.y * 4 + (threadIdx.x >> 5); i < rows; i += gridDim.y * 4) {
-    float mx = neg_inf();
-    for (int k = c + lane; k <= last; k += 32)
-      mx = fmaxf(mx, p.pml[((long long)k * 2 + (k == c ? slot : 0)) * BM + i].x);
-    mx = warp_max(mx);
-    const float ref = mx == neg_inf() ? 0.f : mx;
+    JoinState st;
+    st.begin();
     float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    float l = 0.f;
-    for (int k = c; k <= last; ++k) {
-      const long long at = ((long long)k * 2 + (k == c ? slot : 0)) * BM + i;
-      const float2 ml = p.pml[at];
-      const float w = ex2(ml.x - ref);
-      l += ml.y * w;
+    for (int k0 = c; k0 <= last; k0 += JOIN_AHEAD) {
+      float2 a[JOIN_AHEAD];
+      float4 x[JOIN_AHEAD], y[JOIN_AHEAD];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int d0 = j * 128 + lane * 4;
-        if (d0 < p.d) {
-          const float4 x = *reinterpret_cast<const float4*>(p.po + at * p.d + d0);
-          acc[j].x = fmaf(x.x, w, acc[j].x); acc[j].y = fmaf(x.y, w, acc[j].y);
-          acc[j].z = fmaf(x.z, w, acc[j].z); acc[j].w = fmaf(x.w, w, acc[j].w);
-        }
+      for (int j = 0; j < JOIN_AHEAD; ++j) {
+        const int k = min(k0 + j, last);
+        const long long at = ((long long)k * 2 + (k == c ? slot : 0)) * BM + i;
+        a[j] = p.pml[at];
+        x[j] = *reinterpret_cast<const float4*>(p.po + at * p.d + d0);
+        if (WIDE) y[j] = *reinterpret_cast<const float4*>(p.po + at * p.d + d1);
+      }
+#pragma unroll
+      for (int j = 0; j < JOIN_AHEAD; ++j) {
+        if (k0 + j > last) break;
+        const float2 f = st.add(a[j]);
+        join_add(acc[0], x[j], f);
+        if (WIDE) join_add(acc[1], y[j], f);
       }
     }
     const int row = mt * BM + i, node = row / p.g, qh = h * p.g + row % p.g;
     const long long o = ((long long)b * p.n + node) * p.hq + qh;
-    const float inv = inverse(l);
+    const float inv = inverse(st.l);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int d0 = j * 128 + lane * 4;
-      if (d0 < p.d)
-        store_out(static_cast<T*>(p.out) + o * p.d + d0,
+      const int d = j * 128 + lane * 4;
+      if (d < p.d)
+        store_out(static_cast<T*>(p.out) + o * p.d + d,
                   make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv));
     }
-    if (p.lse && lane == 0) p.lse[o] = lse_of(ref, l);
+    if (p.lse && lane == 0) p.lse[o] = lse_of(st.m == neg_inf() ? 0.f : st.m, st.l);
   }
 }
 

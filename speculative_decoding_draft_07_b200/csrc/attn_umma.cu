@@ -641,7 +641,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 
 // Joins the pieces of the split item that block blockIdx.x began: a thread a row and
 // two 4-column groups (blockIdx.y: 8 groups of 32 rows x 4 of columns, so that a few
-// split items still spread over the device), pieces in unit order, eight loads ahead.
+// split items still spread over the device).
 __global__ void __launch_bounds__(128) attn_umma_join_kernel(AttnParams p, int rows_tile) {
   pdl_wait();
   pdl_trigger();
@@ -650,45 +650,45 @@ __global__ void __launch_bounds__(128) attn_umma_join_kernel(AttnParams p, int r
     for (int b = threadIdx.x; b < p.batch; b += blockDim.x) atomicOr(p.status + b, PCT_DEV_TIMEOUT);
   const int4 m = p.meta[c];
   if (m.x < 0) return;
-  const int b = m.x, h = m.y, mt = m.z, slot = m.w & 1, last = m.w >> 1;
-  const Req r = attn_req(p, b);
-  const int rows = min(p.bm, r.n * p.g - mt * p.bm);
+  const int b = m.x, h = m.y & 1023, rows = m.y >> 10, mt = m.z, slot = m.w & 1, last = m.w >> 1;
   const int place = (blockIdx.y >> 2) * 32 + (threadIdx.x & 31);
   const int w = (blockIdx.y & 3) * 4 + (threadIdx.x >> 5);       // column groups w, w + 16
   const int s = place >> 7, rr = place & 127;
   const int d4 = p.d / 4;
   if (rr >= rows_tile || s * rows_tile + rr >= rows || w >= d4) return;
-  auto ml = [&](int k) { return p.pml[((long long)k * 2 + (k == c ? slot : 0)) * UROWS + place]; };
-  float mx = neg_inf();
-#pragma unroll 8
-  for (int k = c; k <= last; ++k) mx = fmaxf(mx, ml(k).x);
-  const float ref = mx == neg_inf() ? 0.f : mx;
+  JoinState st;
+  st.begin();
   float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  float l = 0.f;
-#pragma unroll 4
-  for (int k = c; k <= last; ++k) {
-    const float2 a = ml(k);
-    const float f = ex2(a.x - ref);
-    l = fmaf(a.y, f, l);
-    const float4* po = reinterpret_cast<const float4*>(p.po) +
-                       ((long long)k * 2 + (k == c ? slot : 0)) * d4 * UROWS + place;
+  const int w1 = w + 16 < d4 ? w + 16 : w;
+  for (int k0 = c; k0 <= last; k0 += JOIN_AHEAD) {
+    float2 a[JOIN_AHEAD];
+    float4 x[JOIN_AHEAD], y[JOIN_AHEAD];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (w + 16 * j < d4) {
-        const float4 x = po[(w + 16 * j) * UROWS];
-        acc[j].x = fmaf(x.x, f, acc[j].x); acc[j].y = fmaf(x.y, f, acc[j].y);
-        acc[j].z = fmaf(x.z, f, acc[j].z); acc[j].w = fmaf(x.w, f, acc[j].w);
-      }
+    for (int j = 0; j < JOIN_AHEAD; ++j) {
+      const int k = min(k0 + j, last);
+      const long long at = (long long)k * 2 + (k == c ? slot : 0);
+      const float4* po = reinterpret_cast<const float4*>(p.po) + at * d4 * UROWS + place;
+      a[j] = p.pml[at * UROWS + place];
+      x[j] = po[w * UROWS];
+      y[j] = po[w1 * UROWS];
+    }
+#pragma unroll
+    for (int j = 0; j < JOIN_AHEAD; ++j) {
+      if (k0 + j > last) break;
+      const float2 f = st.add(a[j]);
+      join_add(acc[0], x[j], f);
+      join_add(acc[1], y[j], f);
+    }
   }
   const int row = mt * p.bm + s * rows_tile + rr, node = row / p.g;
   const long long o = ((long long)b * p.n + node) * p.hq + h * p.g + (row - node * p.g);
-  const float inv = inverse(l);
+  const float inv = inverse(st.l);
 #pragma unroll
   for (int j = 0; j < 2; ++j)
     if (w + 16 * j < d4)
       store_out(static_cast<__nv_bfloat16*>(p.out) + o * p.d + (w + 16 * j) * 4,
                 make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv));
-  if (p.lse && w == 0) p.lse[o] = lse_of(ref, l);
+  if (p.lse && w == 0) p.lse[o] = lse_of(st.m == neg_inf() ? 0.f : st.m, st.l);
 }
 
 bool encode_4d(CUtensorMap* map, const void* base, const cuuint64_t (&dims)[4],
