@@ -286,17 +286,27 @@ __global__ void __launch_bounds__(kF32Threads, F32Shape<DP, WM>::MINB) attn_f32_
           s[j][2 * i + 1] = ex2(s[j][2 * i + 1] - ref[i]);
           l[i] += s[j][2 * i] + s[j][2 * i + 1];
         }
+      // A tile's sum of P V is begun afresh and added to the accumulator by an fp32 add:
+      // the matrix unit cuts its sums off instead of rounding them, which over a long
+      // chain of tiles would add up to one side.
+      PartA a[KW / 8];                                 // keys 2t and 2t + 1 of each eight
 #pragma unroll
       for (int i = 0; i < KW / 8; ++i) {
-        PartA a;                                       // keys 2t and 2t + 1 of the eight
-        a.set(0, __float_as_uint(s[i][0]));
-        a.set(1, __float_as_uint(s[i][2]));
-        a.set(2, __float_as_uint(s[i][1]));
-        a.set(3, __float_as_uint(s[i][3]));
-        const uint32_t* vr = Vs + (wk * KW + i * 8 + 2 * (lane & 3)) * (RB / 4) + (lane >> 2);
+        a[i].set(0, __float_as_uint(s[i][0]));
+        a[i].set(1, __float_as_uint(s[i][2]));
+        a[i].set(2, __float_as_uint(s[i][1]));
+        a[i].set(3, __float_as_uint(s[i][3]));
+      }
+      const uint32_t* vr = Vs + (wk * KW + 2 * (lane & 3)) * (RB / 4) + (lane >> 2);
 #pragma unroll
-        for (int j = 0; j < DP / 8; ++j)
-          mma_f32(acc[j], acc[j], a, split(vr[j * 8]), split(vr[j * 8 + RB / 4]));
+      for (int j = 0; j < DP / 8; ++j) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < KW / 8; ++i)
+          mma_f32(c, c, a[i], split(vr[i * 8 * (RB / 4) + j * 8]),
+                  split(vr[(i * 8 + 1) * (RB / 4) + j * 8]));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[j][q] += c[q];
       }
       if (lost) {                                      // rare: clear the mark for the stage's next tile
         __syncthreads();
