@@ -449,12 +449,12 @@ def _on(t: torch.Tensor, name: str, stream):
     """(device, stream handle, context to allocate and launch in) for work on t's device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    dev = t.device
+    dev, index = t.device, t.get_device()
     if not t.is_cuda:
         raise ValueError(f"{name} is on {dev}, expected a CUDA device")
     if stream is None:
-        if dev.index == torch._C._cuda_getDevice():
-            return dev, torch._C._cuda_getCurrentRawStream(dev.index), _HERE_ALREADY
+        if index == torch._C._cuda_getDevice():
+            return dev, torch._C._cuda_getCurrentRawStream(index), _HERE_ALREADY
         stream = torch.cuda.current_stream(dev)
     elif stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, {name} on {dev}")
@@ -462,10 +462,14 @@ def _on(t: torch.Tensor, name: str, stream):
 
 
 def _want(t: torch.Tensor, name: str, dev: torch.device, shape, dtype):
-    """_check, with the common case first."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.device == dev and t.is_contiguous()):
-        _check(t, name, dev, shape, dtype)
+    """_check, with the common case first (dev is a CUDA device)."""
+    try:
+        if (t.dtype is dtype and t.get_device() == dev.index and t.shape == shape
+                and t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
+    _check(t, name, dev, shape, dtype)
 
 
 def _given(t: Optional[torch.Tensor], name: str, dev: torch.device, shape, dtype) -> torch.Tensor:
@@ -519,18 +523,24 @@ def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, dev: torch.device, max_
            layered: bool = False):
     """_cache_desc of K and V caches [layers][n_pages][page_size][heads][head_dim] (no layer
     axis unless `layered`)."""
-    dims = 5 if layered else 4
+    _same_caches(k_cache, v_cache, dev, 5 if layered else 4)
+    return _cache_desc(k_cache.shape, k_cache.stride(), _code(k_cache), max_pages)
+
+
+def _same_caches(k_cache: torch.Tensor, v_cache: torch.Tensor, dev: torch.device, dims: int):
+    """K and V caches of `dims` axes on dev, of a supported dtype, laid out alike."""
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != dims:
         raise ValueError("k_cache must be a %d-dimensional tensor" % dims)
     if k_cache.device != dev:
         raise ValueError(f"k_cache is on {k_cache.device}, expected {dev}")
+    _code(k_cache)
     shape, stride = k_cache.shape, k_cache.stride()
     if not (isinstance(v_cache, torch.Tensor) and v_cache.dtype is k_cache.dtype
-            and v_cache.device == dev and v_cache.shape == shape and v_cache.stride() == stride):
+            and v_cache.get_device() == dev.index and v_cache.shape == shape
+            and v_cache.stride() == stride):
         st = _view(v_cache, "v_cache", dev, shape, k_cache.dtype)
         if list(st) != list(_strides(shape, stride, "k_cache")):
             raise ValueError("k_cache and v_cache must have the same strides")
-    return _cache_desc(shape, stride, _code(k_cache), max_pages)
 
 
 def kv_pages_resize(ctx_len: torch.Tensor, block_table: torch.Tensor, held: torch.Tensor,
@@ -627,6 +637,19 @@ def _attn_workspace(shape, stride, code: int, max_pages: int, batch: int, n_stri
                                               n_stride, heads_q))
 
 
+@functools.lru_cache(maxsize=1024)
+def _attn_plan(q_shape, q_stride, shape, stride, dtype, max_pages: int, device: int):
+    """(reference to the cache's descriptor, query strides, workspace bytes) of an attention
+    call, which the shapes and strides of its tensors alone decide."""
+    code = PCT_BF16 if dtype is torch.bfloat16 else PCT_F32
+    _, ref, _ = _cache_desc(shape, stride, code, max_pages)
+    batch, n, hq, _ = q_shape
+    nbytes = _attn_workspace(shape, stride, code, max_pages, batch, n, hq, device)
+    if nbytes == 0:
+        _raise(PCT_EINVAL, "tree_attention_workspace")
+    return ref, _strides(q_shape, q_stride, "q"), nbytes
+
+
 def tree_attention_workspace(k_cache: torch.Tensor, v_cache: torch.Tensor, max_pages: int,
                              batch: int, n_stride: int, heads_q: int) -> int:
     """Workspace bytes tree_attention needs for these shapes on the current device."""
@@ -654,8 +677,11 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     rows, max_pages = _rows(block_table, "block_table", dev, _I32)
     if rows != batch:
         raise ValueError(f"block_table has {rows} rows, expected {batch}")
-    desc, ref, _ = _cache(k_cache, v_cache, dev, max_pages)
-    st = _view(q, "q", dev, (batch, n, hq, desc.head_dim), k_cache.dtype)
+    _same_caches(k_cache, v_cache, dev, 4)
+    if q.dtype is not k_cache.dtype or k_cache.shape[3] != d:
+        _view(q, "q", dev, (batch, n, hq, k_cache.shape[3]), k_cache.dtype)
+    ref, st, nbytes = _attn_plan(q.shape, q.stride(), k_cache.shape, k_cache.stride(), q.dtype,
+                                 max_pages, q.get_device())
     _want(ctx_len, "ctx_len", dev, (batch,), _I64)
     if count is not None:
         _want(count, "count", dev, (batch,), _I32)
@@ -671,10 +697,6 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
             if out.lse is not None:
                 _want(out.lse, "out.lse", dev, (batch, n, hq), _F32)
             _want(out.status, "out.status", dev, (batch,), _I32)
-        nbytes = _attn_workspace(k_cache.shape, k_cache.stride(), desc.dtype, max_pages, batch, n,
-                                 hq, dev.index)
-        if nbytes == 0:
-            _raise(PCT_EINVAL, "tree_attention_workspace")
         ws, wsb = _workspace(nbytes, dev, workspace)
         code = lib().tree_attention(ref, batch, n, hq, d ** -0.5 if scale is None else scale,
                                     q.data_ptr(), st, k_cache.data_ptr(), v_cache.data_ptr(),

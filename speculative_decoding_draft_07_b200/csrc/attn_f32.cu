@@ -82,7 +82,9 @@ __global__ void __launch_bounds__(kF32Threads, F32Shape<DP, WM>::MINB) attn_f32_
   unsigned char* ring = smem + BM * RB;                // [STAGES][K, V][BK][PITCH]
   float* obuf = reinterpret_cast<float*>(ring);        // [WK][BM][DP + 8] at an item's end
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wm = warp % WM, wk = warp / WM;
+  __shared__ int lost_page;
   if (tid < 4) gone[tid] = 0;
+  if (tid == 0) lost_page = 0;
   pdl_wait();
   pdl_trigger();
   sched_begin<BK, NT>(p, &share, sums);
@@ -108,8 +110,10 @@ __global__ void __launch_bounds__(kF32Threads, F32Shape<DP, WM>::MINB) attn_f32_
         const int page = __ldg(table + col);
         if (page >= 0 && page < p.n_pages)
           off = page * p.ks_page + (tok - (int)col * p.page_size) * p.ks_slot;
-        else
+        else {
           atomicOr(&gone[t & 3], 1ull << tid);
+          lost_page = FAIL_PAGE;
+        }
       }
       where[t & 3][tid] = off;
     };
@@ -364,8 +368,12 @@ __global__ void __launch_bounds__(kF32Threads, F32Shape<DP, WM>::MINB) attn_f32_
       }
     }
   }
-  if (tid == 0) p.meta[blockIdx.x] = begun;
-  attn_tail<float>(p);
+  attn_zero<float>(p, tid, NT);
+  __syncthreads();
+  if (tid == 0) {
+    p.meta[blockIdx.x] = begun;
+    p.fail[blockIdx.x] = lost_page;
+  }
 }
 
 template <int DP, int WM>

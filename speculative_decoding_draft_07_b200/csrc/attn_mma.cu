@@ -61,7 +61,9 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<DP>::MINB) attn_mma_kern
   unsigned char* ring = smem + BM * DP * 2;            // [STAGES][K, V][BK][DP]
   float* obuf = reinterpret_cast<float*>(ring);        // [WK][BM][DP + 8] at an item's end
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wm = warp % WM, wk = warp / WM;
+  __shared__ int lost_page;
   if (tid < 4) gone[tid] = 0;
+  if (tid == 0) lost_page = 0;
   pdl_wait();
   pdl_trigger();
   sched_begin<BK, NT>(p, &share, sums);
@@ -87,8 +89,10 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<DP>::MINB) attn_mma_kern
         const int page = __ldg(table + col);
         if (page >= 0 && page < p.n_pages)
           off = page * p.ks_page + (tok - (int)col * p.page_size) * p.ks_slot;
-        else
+        else {
           atomicOr(&gone[t & 3], 1ull << tid);
+          lost_page = FAIL_PAGE;
+        }
       }
       where[t & 3][tid] = off;
     };
@@ -313,8 +317,12 @@ __global__ void __launch_bounds__(kMmaThreads, MmaShape<DP>::MINB) attn_mma_kern
       }
     }
   }
-  if (tid == 0) p.meta[blockIdx.x] = begun;
-  attn_tail<__nv_bfloat16>(p);
+  attn_zero<__nv_bfloat16>(p, tid, NT);
+  __syncthreads();
+  if (tid == 0) {
+    p.meta[blockIdx.x] = begun;
+    p.fail[blockIdx.x] = lost_page;
+  }
 }
 
 template <int DP, int WM>

@@ -31,7 +31,7 @@ struct AttnParams {
   int32_t* status;
   float* po;                    // [grid][2][bm][d] pieces' sums
   float2* pml;                  // [grid][2][bm] pieces' (maximum in log2 units, sum)
-  int32_t* fail;                // [grid] set by a block whose bounded wait gave up (attn_umma)
+  int32_t* fail;                // [grid] FAIL_* bits of each block
   int bm;                       // rows of an item
   int half;                     // units: `few` a tile of an item with at most this many
   int few, many, per_item;      // rows, `many` of one with more, `per_item` an item
@@ -227,28 +227,45 @@ __device__ void sched_begin(const AttnParams& p, Share* out, long long* sums) {
   __syncthreads();
 }
 
-// Rows at or past count (and all rows of a refused request) to 0 and -inf, and
-// the status word, for requests blockIdx.x, blockIdx.x + grid, ...
+// Rows at or past count (and all rows of a refused request) to 0 and -inf. Requests
+// are spread over the grid, several blocks a request where there are more blocks.
 template <typename T>
-__device__ void attn_tail(const AttnParams& p) {
-  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+__device__ void attn_zero(const AttnParams& p, int tid, int threads) {
+  const int parts = max(1, (int)gridDim.x / p.batch);
+  for (int task = blockIdx.x; task < p.batch * parts; task += gridDim.x) {
+    const int b = task % p.batch, part = task / p.batch;
     const Req r = attn_req(p, b);
-    const int32_t* row = p.table + (long long)b * p.max_pages;
-    int bad = 0;
-    if (r.n > 0) {
-      const int e = (int)((r.ctx + r.n - 1) / p.page_size);
-      for (int k = threadIdx.x; k <= e; k += blockDim.x)
-        bad |= row[k] < 0 || row[k] >= p.n_pages;
-    }
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) p.status[b] = r.st | (bad ? PCT_DEV_BAD_PAGE : 0);
     const long long r0 = ((long long)b * p.n + r.n) * p.hq, r1 = ((long long)b * p.n + p.n) * p.hq;
     const int vec = p.d * (int)sizeof(T) / 16;
     uint4* o = static_cast<uint4*>(p.out);
-    for (long long i = r0 * vec + threadIdx.x; i < r1 * vec; i += blockDim.x)
+    for (long long i = r0 * vec + part * threads + tid; i < r1 * vec; i += (long long)parts * threads)
       o[i] = make_uint4(0, 0, 0, 0);
     if (p.lse)
-      for (long long i = r0 + threadIdx.x; i < r1; i += blockDim.x) p.lse[i] = neg_inf();
+      for (long long i = r0 + part * threads + tid; i < r1; i += (long long)parts * threads)
+        p.lse[i] = neg_inf();
+  }
+}
+
+// A block's report in p.fail.
+constexpr int FAIL_TIMEOUT = 1, FAIL_PAGE = 2;
+
+// Status words, by the join: block tables are looked over again only if some block
+// met a bad page. All threads of the blocks with blockIdx.y == 0 call it.
+__device__ __forceinline__ void attn_status(const AttnParams& p) {
+  int any = 0;
+  for (int i = threadIdx.x; i < (int)gridDim.x; i += blockDim.x) any |= p.fail[i];
+  const int late = __syncthreads_or(any & FAIL_TIMEOUT), page = __syncthreads_or(any & FAIL_PAGE);
+  for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
+    const Req r = attn_req(p, b);
+    int bad = 0;
+    if (page && r.n > 0) {
+      const int32_t* row = p.table + (long long)b * p.max_pages;
+      const int e = (int)((r.ctx + r.n - 1) / p.page_size);
+      for (int k = threadIdx.x; k <= e; k += blockDim.x) bad |= row[k] < 0 || row[k] >= p.n_pages;
+    }
+    if (page) bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0)
+      p.status[b] = r.st | (bad ? PCT_DEV_BAD_PAGE : 0) | (late ? PCT_DEV_TIMEOUT : 0);
   }
 }
 
@@ -304,6 +321,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnParams p) {
   pdl_trigger();
   const int c = blockIdx.x;
   const int4 m = p.meta[c];
+  if (blockIdx.y == 0) attn_status(p);
   if (m.x < 0) return;
   const int b = m.x, h = m.y & 1023, rows = m.y >> 10, mt = m.z, slot = m.w & 1, last = m.w >> 1;
   const int lane = threadIdx.x & 31;

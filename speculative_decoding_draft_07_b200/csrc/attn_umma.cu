@@ -201,6 +201,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     int4 begun = make_int4(-1, 0, 0, 0);
     bool ok = true;
     uint32_t armed = 0;                              // ring slots used
+    bool lost_page = false;
     int slot = 0;
     uint32_t par = 0;
     const int boxes = UBK >> mp.shift;               // boxes of a tile
@@ -256,6 +257,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
         const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
         const uint32_t lost = __ballot_sync(0xffffffffu, live && page < 0);
+        lost_page |= lost != 0;
         if (lane == 0) {
           uint32_t g[2] = {0, 0};
           for (int i = 0; lost >> i; ++i)
@@ -283,7 +285,10 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
       seq0 += t1 - t0;
     }
-    if (lane == 0) p.meta[blockIdx.x] = begun;
+    if (lane == 0) {
+      p.meta[blockIdx.x] = begun;
+      if (lost_page) atomicOr(err, FAIL_PAGE);
+    }
     // every copy has landed before the block may exit: slot i was last armed in the
     // current round when i < slot, in the one before otherwise
 #pragma unroll
@@ -378,7 +383,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           if (*abort_flag) break;
           if (clock64() - c0 > kTimeoutCycles) {
             *abort_flag = 1;
-            atomicExch(err, 1);
+            atomicOr(err, FAIL_TIMEOUT);
             break;
           }
         }
@@ -427,6 +432,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const uint32_t aS = tS + s * 128 + lane_base, aO = tO + s * DP + lane_base;
     const float c = p.scale_log2;
     int n = 0, n_items = 0;                              // tiles of this stream, items
+    attn_zero<__nv_bfloat16>(p, s * 128 + tl, 256);      // while the first tiles arrive
     uint32_t met = 0;
     auto wait = [&](uint64_t* bar, uint32_t par) {
       const bool got = wait_bar(bar, par, abort_flag, err);
@@ -636,7 +642,6 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tS), "r"(512));
   }
-  attn_tail<__nv_bfloat16>(p);
 }
 
 // Joins the pieces of the split item that block blockIdx.x began: a thread a row and
@@ -646,9 +651,8 @@ __global__ void __launch_bounds__(128) attn_umma_join_kernel(AttnParams p, int r
   pdl_wait();
   pdl_trigger();
   const int c = blockIdx.x;
-  if (blockIdx.y == 0 && p.fail[c])
-    for (int b = threadIdx.x; b < p.batch; b += blockDim.x) atomicOr(p.status + b, PCT_DEV_TIMEOUT);
   const int4 m = p.meta[c];
+  if (blockIdx.y == 0) attn_status(p);
   if (m.x < 0) return;
   const int b = m.x, h = m.y & 1023, rows = m.y >> 10, mt = m.z, slot = m.w & 1, last = m.w >> 1;
   const int place = (blockIdx.y >> 2) * 32 + (threadIdx.x & 31);

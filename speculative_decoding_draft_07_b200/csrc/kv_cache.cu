@@ -227,6 +227,7 @@ struct RowGeom {
 // per piece (with two of 64 bits each, 32 x 1000 tokens of 8 x 128 bf16 took 63 us).
 constexpr int kAppendRows = 32;
 constexpr int kAppendLoads = 8;
+constexpr int kAppendScan = 2048;
 __global__ void __launch_bounds__(256)
 kv_append_kernel(RowGeom g, int batch, int n_stride, long long n_slots, int cols,
                  const uint4* __restrict__ k_new, const uint4* __restrict__ v_new, long long s_b,
@@ -268,12 +269,19 @@ kv_append_kernel(RowGeom g, int batch, int n_stride, long long n_slots, int cols
       }
     }
   }
-  for (int b = blockIdx.x; b < batch; b += gridDim.x) {
-    int bad = 0;
-    for (int i = tid; i < n_stride; i += blockDim.x)
-      bad |= slot[(long long)b * n_stride + i] >= n_slots;
-    bad = __syncthreads_or(bad);
-    if (tid == 0) status[b] = bad ? PCT_DEV_BAD_PAGE : 0;
+  // status words: short requests by one block each, long ones (already zero) by
+  // whichever block holds the bad slot
+  if (n_stride <= kAppendScan) {
+    for (int b = blockIdx.x; b < batch; b += gridDim.x) {
+      int bad = 0;
+#pragma unroll 4
+      for (int i = tid; i < n_stride; i += 256)
+        bad |= slot[(long long)b * n_stride + i] >= n_slots;
+      bad = __syncthreads_or(bad);
+      if (tid == 0) status[b] = bad ? PCT_DEV_BAD_PAGE : 0;
+    }
+  } else if (tid < kAppendRows && r0 + tid < rows && slot[r0 + tid] >= n_slots) {
+    atomicOr(status + (r0 + tid) / n_stride, PCT_DEV_BAD_PAGE);
   }
 }
 
@@ -396,6 +404,10 @@ cudaError_t launch_kv_append(const kv_cache_desc& d, int batch, int n_stride, co
   const int per = d.dtype == PCT_BF16 ? 8 : 4;
   const int cols = g.heads * g.vec * 2 < 256 ? g.heads * g.vec * 2 : 256;   // columns a pass
   const long long grid = ((long long)batch * n_stride + kAppendRows - 1) / kAppendRows;
+  if (n_stride > kAppendScan) {
+    const cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int32_t) * batch, s);
+    if (e != cudaSuccess) return e;
+  }
   kv_append_kernel<<<(unsigned)grid, 256, 0, s>>>(
       g, batch, n_stride, (long long)d.n_pages * d.page_size, cols,
       static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), new_stride[0] / per,

@@ -73,15 +73,13 @@ cudaError_t launch_attn(const AttnArgs& a, void* ws, cudaStream_t s) {
   p.po = reinterpret_cast<float*>(w + P.o_po);
   p.pml = reinterpret_cast<float2*>(w + P.o_ml);
   p.meta = reinterpret_cast<int4*>(w + P.o_meta);
-  p.fail = nullptr;
+  p.fail = reinterpret_cast<int32_t*>(w + P.o_fail);
   p.bm = p.half = P.bm;
   p.few = p.many = 1;
   p.per_item = 0;
   // the tcgen05 kernel scales masked (-inf) scores and takes maxima before scaling
   if (P.umma && a.scale > 0.f) {
-    AttnParams up = p;
-    up.fail = reinterpret_cast<int32_t*>(w + P.o_fail);
-    const cudaError_t e = launch_attn_umma(up, num_sms(), s);
+    const cudaError_t e = launch_attn_umma(p, num_sms(), s);
     if (e != cudaErrorNotSupported) return e;   // strides a tensor map cannot hold: the other kernel
   }
   return a.kv.dtype == PCT_BF16 ? launch_attn_mma(p, P.bm, P.grid, s)

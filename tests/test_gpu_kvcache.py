@@ -398,7 +398,7 @@ def test_tree_slots_match_the_oracle(B, n, page):
 # rows into the cache, and the accepted path's rows
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("B,n,hkv,d,page,layout", [(1, 1, 1, 8, 16, "nhd"), (3, 7, 2, 64, 5, "hnd"), (4, 50, 8, 128, 16, "kv"),
-                                                   (2, 300, 3, 72, 64, "nhd")])
+                                                   (2, 300, 3, 72, 64, "nhd"), (3, 2500, 1, 64, 16, "nhd")])
 def test_append_matches_the_oracle(B, n, hkv, d, page, layout, dtype):
     torch.manual_seed(B)
     rng = np.random.default_rng(n)
