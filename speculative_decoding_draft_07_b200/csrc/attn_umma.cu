@@ -645,8 +645,8 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 }
 
 // Joins the pieces of the split item that block blockIdx.x began: a thread a row and
-// two 4-column groups (blockIdx.y: 8 groups of 32 rows x 4 of columns, so that a few
-// split items still spread over the device).
+// two 4-column groups (blockIdx.y: 8 groups of 32 rows x 4 of columns; one request of 64
+// nodes over 8000 tokens takes 46, 41, 37 and 42 us with 1, 2, 4 and 8 of columns).
 __global__ void __launch_bounds__(128) attn_umma_join_kernel(AttnParams p, int rows_tile) {
   pdl_wait();
   pdl_trigger();
