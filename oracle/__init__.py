@@ -28,6 +28,10 @@ pages define, written step by step in their order and notation:
   (CaDDTree summary, "Method": convex, non-decreasing cost profiled offline),
   by exhaustive search over the 16 free sets.
 
+* ``kvcache`` -- the paged key-value cache around the target's forward (block
+  tables, slots, appended and committed rows) and attention of a tree's nodes over
+  it with the ancestor mask.
+
 Parity status of each function (what pins it, other than itself, is in
 ``tests/test_oracle_*.py``):
 
@@ -61,6 +65,7 @@ from .caddtree import cadd_tree_grow, CaddResult, cadd_cost, row_topk
 from .verify import tree_verify_accept, tree_ancestor_mask, VerifyResult
 from .accept_sim import accept_sim, philox4x32_10, uniform24
 from .costfit import cost_fit
+from . import kvcache
 
 __all__ = [
     "decode_bf16", "to_f64", "row_log_softmax",
@@ -68,5 +73,5 @@ __all__ = [
     "cadd_tree_grow", "CaddResult", "cadd_cost",
     "tree_verify_accept", "tree_ancestor_mask", "VerifyResult",
     "accept_sim", "philox4x32_10", "uniform24",
-    "cost_fit",
+    "cost_fit", "kvcache",
 ]

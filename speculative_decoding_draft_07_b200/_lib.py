@@ -697,6 +697,8 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
             if out.lse is not None:
                 _want(out.lse, "out.lse", dev, (batch, n, hq), _F32)
             _want(out.status, "out.status", dev, (batch,), _I32)
+        if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+            raise ValueError(f"workspace must be contiguous on {dev}")
         ws, wsb = _workspace(nbytes, dev, workspace)
         code = lib().tree_attention(ref, batch, n, hq, d ** -0.5 if scale is None else scale,
                                     q.data_ptr(), st, k_cache.data_ptr(), v_cache.data_ptr(),

@@ -54,7 +54,7 @@ __device__ __forceinline__ Req attn_req(const AttnParams& p, int b) {
   r.n = p.count ? p.count[b] : p.n;
   r.st = 0;
   if (r.n < 0 || r.n > p.n) r.st |= PCT_DEV_BAD_COUNT;
-  if (r.ctx < 0 || (r.st == 0 && r.ctx + r.n > (long long)p.max_pages * p.page_size))
+  if (r.ctx < 0 || (r.st == 0 && r.ctx > (long long)p.max_pages * p.page_size - r.n))
     r.st |= PCT_DEV_BAD_LENGTH;
   if (r.st) { r.n = 0; r.ctx = 0; }
   return r;

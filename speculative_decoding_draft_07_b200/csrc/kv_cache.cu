@@ -65,10 +65,9 @@ kv_pages_resize_kernel(int batch, int page_size, int max_pages, int n_pages,
     if (b >= batch) return 0;
     const long long c = ctx_len[b], n = count ? (long long)count[b] : 0;
     const int h = held[b];
-    const long long t = c + n, w = (t + page_size - 1) / page_size;
-    if (c < 0 || n < 0 || c > (1ll << 31) || w > max_pages || h < 0 || h > max_pages)
+    if (c < 0 || n < 0 || c > (long long)max_pages * page_size - n || h < 0 || h > max_pages)
       return PCT_DEV_BAD_LENGTH;
-    want = (int)w;
+    want = (int)((c + n + page_size - 1) / page_size);
     have = h;
     return 0;
   };
@@ -185,7 +184,7 @@ kv_tree_slots_kernel(int n_stride, int page_size, int max_pages, int n_pages,
   const long long c = ctx_len[b];
   int n = count ? count[b] : n_stride, st = 0;
   if (n < 0 || n > n_stride) st |= PCT_DEV_BAD_COUNT;
-  if (c < 0 || (st == 0 && c + n > (long long)max_pages * page_size)) st |= PCT_DEV_BAD_LENGTH;
+  if (c < 0 || (st == 0 && c > (long long)max_pages * page_size - n)) st |= PCT_DEV_BAD_LENGTH;
   if (st) n = 0;
   const int32_t* row = block_table + (long long)b * max_pages;
   if (i < n_stride) {
@@ -307,7 +306,7 @@ kv_commit_kernel(RowGeom g, long long s_layer, int layers, int max_depth, int ma
   const int32_t* row = block_table + (long long)b * max_pages;
   int st = 0;
   if (n < 1) st |= PCT_DEV_BAD_COUNT;
-  else if (c < 0 || c + n > (long long)max_pages * g.page_size) st |= PCT_DEV_BAD_LENGTH;
+  else if (c < 0 || c > (long long)max_pages * g.page_size - n) st |= PCT_DEV_BAD_LENGTH;
   if (a < 0 || a > max_depth) st |= PCT_DEV_BAD_PATH;
   if (st == 0) {
     int bad = 0;

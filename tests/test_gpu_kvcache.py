@@ -120,7 +120,8 @@ SHAPES = [
     dict(n=12, ctx=(40, 3), hq=1, hkv=1, d=8, page=4), dict(n=40, ctx=(0, 12, 100), mask="random", d=128),
     dict(n=100, ctx=(0, 129), mask="random", hq=8, hkv=4, page=128, d=128),
     dict(n=9, ctx=(8, 30, 64, 0), counts=[9, 0, 1, 4]), dict(n=70, ctx=(513, 127, 0), counts=[70, 3, 64], hq=8, hkv=2, d=128, page=128),
-    dict(n=3, ctx=(60,), hq=64, hkv=1, d=64),
+    dict(n=3, ctx=(60,), hq=64, hkv=1, d=64), dict(n=5, ctx=(90, 0), hq=48, hkv=1, d=128),
+    dict(n=400, ctx=(150, 0), hq=2, hkv=1, d=64, mask=None), dict(n=50, ctx=(200, 3), hq=2, hkv=2, d=112, page=8),
 ]
 
 
@@ -220,6 +221,33 @@ def test_refused_requests_and_bad_pages():
     r = _run(g)
     ref = _check(r, g, table, ctx, counts, m)
     assert ref.status.tolist() == [okv.BAD_COUNT, okv.BAD_LENGTH, okv.BAD_LENGTH, okv.BAD_PAGE, okv.BAD_COUNT]
+
+
+def test_lengths_far_outside_are_refused():
+    """Lengths at the ends of 64 bits: every call answers PCT_DEV_BAD_LENGTH and touches nothing of the request."""
+    far = [2 ** 63 - 1, -2 ** 63, 2 ** 62, 2 ** 32 + 5, 5]
+    c = _case(14, n=4, ctx=(5,) * 5)
+    g, table = c[0], c[1]
+    g["ctx"].copy_(torch.tensor(far))
+    r = _run(g)
+    slot, pos, st = pct.kv_tree_slots(g["ctx"], g["count"], g["table"], 4, 16, g["k"].shape[0])
+    before = g["k"].clone()
+    new_len, st2 = pct.kv_commit(g["k"], g["v"], g["table"], g["ctx"], g["count"],
+                                 torch.full((5,), 1, dtype=torch.int32, device=DEV),
+                                 torch.full((5, 2), 2, dtype=torch.int32, device=DEV))
+    want, held, free, nfree = g["table"].clone(), *(torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([1] * 5, list(range(99)), [0]))
+    st3 = pct.kv_pages_resize(g["ctx"], g["table"], held, free, nfree, 16, count=g["count"])
+    torch.cuda.synchronize()
+    for s in (r.status, st, st2, st3):
+        assert host(s).tolist() == [okv.BAD_LENGTH] * 4 + [0]
+    assert (r.out[:4] == 0).all() and torch.isneginf(r.lse[:4]).all() and (r.out[4] != 0).any()
+    assert (slot[:4] == -1).all() and (pos[:4] == -1).all() and host(new_len).tolist() == far[:4] + [7]
+    assert torch.equal(g["table"][:4], want[:4]) and torch.equal(host_rows(g["k"], table, 4), host_rows(before, table, 4))
+
+
+def host_rows(k, table, requests):
+    used = torch.from_numpy(table[:requests][table[:requests] >= 0].astype(np.int64)).to(DEV)
+    return k[used]
 
 
 @pytest.mark.parametrize("dtype,n,hq,batch", [("bf16", 1, 8, 300), ("bf16", 70, 16, 3), ("f32", 5, 8, 40)])
