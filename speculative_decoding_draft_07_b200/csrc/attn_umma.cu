@@ -569,17 +569,17 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       if (!split) {
         const float f = whole ? inverse(l) : 1.f;
 #pragma unroll
-        for (int j = 0; j < DP / 16; ++j) {
-          uint32_t o[16];
+        for (int j = 0; j < DP / 64; ++j) {
+          uint32_t o[64];
           __syncwarp();
-          tmem_issue(aO + j * 16, o);
+          tmem_issue(aO + j * 64, o);
           tmem_wait(o);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int q = 0; q < 8; ++q) {
             float y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(o[q * 8 + e]) * f;
-            put(j * 16 + q * 8, y);
+            put(j * 64 + q * 8, y);
           }
         }
       } else {
@@ -601,15 +601,15 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const float f = whole ? inverse(row_l) : 1.f;
         const uint32_t a0 = tO + lane_base + col0;
 #pragma unroll
-        for (int j = 0; j < DP / 32; ++j) {
-          uint32_t o[16], o2[16];
+        for (int j = 0; j < DP / 64; ++j) {
+          uint32_t o[32], o2[32];
           __syncwarp();
-          tmem_issue(a0 + j * 16, o);
-          tmem_issue(a0 + DP + j * 16, o2);
+          tmem_issue(a0 + j * 32, o);
+          tmem_issue(a0 + DP + j * 32, o2);
           tmem_wait(o);
           tmem_wait(o2);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
+          for (int q = 0; q < 4; ++q) {
             float y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -617,7 +617,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
               if (two) y[e] = fmaf(__uint_as_float(o2[q * 8 + e]), fb, y[e]);
               y[e] *= f;
             }
-            put(col0 + j * 16 + q * 8, y);
+            put(col0 + j * 32 + q * 8, y);
           }
         }
         tc_fence_before();
