@@ -6,7 +6,7 @@
 // as two streams:
 //   * warp 0: TMA producer. Publishes the items, loads their queries (double
 //     buffered) and streams K and V tiles through a ring of 128-byte swizzled
-//     slots, each page of a tile its own box (a lane a page);
+//     slots, a lane a box (a page's tokens in the tile, or 8, 16 or 32 of them);
 //   * warps 1 and 2, one thread each: issue S = Q K^T (shared x shared) and O += P V
 //     (P from tensor memory) of stream 0 and 1. A stream's scores are double
 //     buffered, so its next S runs under the softmax of the current one. Two
@@ -60,7 +60,7 @@ template <int DP> struct UShape {
 };
 
 struct UMaps {
-  int shift;                             // log2 of a box's tokens (a page, at most 64)
+  int shift;                             // log2 of a box's tokens
   int slot_dim;                          // cache map axis of the token in a page: 1 or 2
   int rows;                              // R
 };
@@ -707,7 +707,7 @@ bool encode_4d(CUtensorMap* map, const void* base, const cuuint64_t (&dims)[4],
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // [n_pages][heads][page places][d]; the place and the head in order of their strides.
-// Boxes of 64 columns x min(page, 64) places. (An axis of one entry is never
+// Boxes of 64 columns x `rows` places. (An axis of one entry is never
 // stepped over: any valid stride will do for it.)
 bool encode_cache(CUtensorMap* map, const void* base, const AttnParams& p, int rows, int* slot_dim) {
   const cuuint64_t row = (cuuint64_t)(p.d * 2 + 15) / 16 * 16;
@@ -757,17 +757,17 @@ cudaError_t run_umma(const AttnParams& p, const CUtensorMap& q, const CUtensorMa
 
 int attn_umma_rows() { return UROWS; }
 
-// Pages whose rows fill a swizzled tile without straddling it: a divisor of 64
-// from 8 rows (the swizzle's period) up, or a multiple of 64.
-bool attn_umma_pages(int page_size) {
-  return page_size % UBK == 0 || (page_size >= 8 && UBK % page_size == 0);
-}
+// A box holds the largest power of two of tokens that divides the page, at most a
+// tile: it never straddles a page, and from 8 rows on (the swizzle's period) it keeps
+// the tile's layout.
+int box_rows(int page_size) { return std::min(page_size & -page_size, UBK); }
+bool attn_umma_pages(int page_size) { return box_rows(page_size) >= 8; }
 
 // cudaErrorNotSupported when the strides do not fit a tensor map.
 cudaError_t launch_attn_umma(AttnParams p, int grid, cudaStream_t s) {
   CUtensorMap q, k, v, o;
   UMaps mp;
-  const int rows = std::min(p.page_size, UBK);
+  const int rows = box_rows(p.page_size);
   mp.shift = 0;
   while ((1 << mp.shift) < rows) ++mp.shift;
   const int nodes = 128 / p.g;
