@@ -388,7 +388,7 @@ int32_t tree_verify_accept_noalloc(int32_t batch, int32_t n_stride, int32_t voca
  * PCT_EINVAL); head_dim is a multiple of 8 in 8..256. Offsets are 64-bit.
  * Block tables are [batch][max_pages] int32; entries past a request's pages are
  * never read. A request uses a page at most once, no two requests write the
- * same page, and the calls do not check that.
+ * same page, and the calls do not check that. Outputs do not overlap inputs.
  * ------------------------------------------------------------------------ */
 typedef struct {
   int32_t n_pages;      /* pages of the cache, >= 1                                  */

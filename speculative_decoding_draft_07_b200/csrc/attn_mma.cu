@@ -1,8 +1,10 @@
 // Tree attention for bf16 caches and few rows, any page size (mma.sync).
 //
-// With up to 64 rows (nodes x query heads of a group) against each key, every
-// K and V element takes part in at most 64 products, so the cache's bytes bound
-// the kernel and the warp-level matrix instructions keep up. A block of four
+// It takes calls of up to 32 rows (nodes x query heads of a group) a KV head, and
+// larger ones whose pages (no multiple of 8 tokens), strides or scale (not positive)
+// the tcgen05 kernel cannot take. With so few rows against each key the cache's bytes
+// bound it and the warp-level matrix instructions keep up: 32 decode requests over up
+// to 32768 tokens, 8 heads of 128, 331 us (6.8 TB/s). A block of four
 // warps is WM x WK: WM warps of 16 rows each, the others splitting the keys of a
 // tile (one row group: four warps on 16 keys each). Every warp keeps its own
 // running maximum, sum and 16 x head_dim accumulator in registers; they meet only

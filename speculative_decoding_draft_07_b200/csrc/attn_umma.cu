@@ -20,7 +20,8 @@
 //   * warp 11: stores these rows by TMA (boxes like the queries'; rows past count
 //     are staged as zeros) and hands the buffer back to the producer. With the
 //     softmax warps storing them an item cost as much as 5.6 tiles.
-// With more than R rows in an item the streams are its two row tiles and share
+// (head_dim above 128: one stream and one row tile, whose accumulator takes half of
+// tensor memory.) With more than R rows in an item the streams are its two row tiles and share
 // every K and V tile; with fewer they take alternate key tiles of the same rows
 // and are added up at the item's end (both accumulators sit in the same tensor
 // memory lanes). Tensor memory: S (2 streams x 2 buffers x 64 columns, P in the
@@ -29,7 +30,9 @@
 // seldom do; weights up to 2^8 lose nothing in fp32 sums and bf16 products.
 // 64 tokens a tile rather than 128: with 128 the scores fill tensor memory once
 // (head_dim 128), so that S, softmax and P V of a stream run one after another
-// (64 requests x 256 nodes over up to 4096 tokens: 1.41 ms).
+// (64 requests x 256 nodes over up to 4096 tokens: 1.41 ms; this takes 0.81-0.88,
+// 630-680 TFLOP/s). A 64-token tile of both streams takes about 2000 cycles, 1270 of
+// products alone and 1024 of exponentials, which overlap in part.
 // Every mbarrier wait is bounded; when one gives up, the roles run to the end
 // without waiting, drain their copies and products, free the tensor memory, and
 // the join reports PCT_DEV_TIMEOUT.
@@ -50,13 +53,14 @@ constexpr int GONE = 8;                  // tiles whose bad-page marks are kept
 constexpr int ITEMS = 4;                 // published items
 
 template <int DP> struct UShape {
+  static constexpr int STREAMS = DP == 256 ? 1 : 2;        // (two accumulators fill tensor memory)
   static constexpr int HALVES = DP / 64;                   // 64-column boxes of a row
   static constexpr int QHALF = 128 * 128;                  // bytes of 128 rows of a box
   static constexpr int QTILE = HALVES * QHALF;
   static constexpr int KHALF = UBK * 128;
   static constexpr int SLOT = HALVES * KHALF;
-  static constexpr int SLOTS = DP == 128 ? 6 : 8;          // K and V tiles in flight
-  static constexpr size_t SMEM = 1024 + 4 * QTILE + SLOTS * SLOT;
+  static constexpr int SLOTS = DP == 256 ? 3 : DP == 128 ? 6 : 8;   // K and V tiles in flight
+  static constexpr size_t SMEM = 1024 + 2 * STREAMS * QTILE + SLOTS * SLOT;
 };
 
 struct UMaps {
@@ -143,10 +147,11 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                  const AttnParams p, const UMaps mp) {
   typedef UShape<DP> U;
+  constexpr int STREAMS = U::STREAMS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sQ = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));   // [stream][2]
-  uint8_t* ring = sQ + 4 * U::QTILE;
+  uint8_t* ring = sQ + 2 * STREAMS * U::QTILE;
   __shared__ uint64_t full[U::SLOTS], empty[U::SLOTS], qfull[2][2], qempty[2][2], sfull[2][2],
       pready[2][2], pvdone[2][2], staged[2][2], item_full[ITEMS], pair, drain[2];
   __shared__ Item items[ITEMS];
@@ -160,7 +165,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   int32_t* err = p.fail + blockIdx.x;
 
   if (tid == 0) {
-    for (int i = 0; i < U::SLOTS; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 2); }
+    for (int i = 0; i < U::SLOTS; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], STREAMS); }
     for (int i = 0; i < 2; ++i) {
       for (int j = 0; j < 2; ++j) {
         mbar_init(&qfull[i][j], 1);
@@ -212,7 +217,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const int buf = n_items & 1;
       const uint32_t qpar = (uint32_t)(n_items >> 1) & 1u;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
+      for (int s = 0; s < STREAMS; ++s) {
         // the buffer's reader is done, and so is the copy before (a stream without
         // tiles does not wait for its queries)
         bool got = wait_bar(&qempty[s][buf], qpar ^ 1u, abort_flag, err);
@@ -220,7 +225,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (!__all_sync(0xffffffffu, got)) ok = false;
       }
       if (!ok) break;
-      const bool split = rows <= mp.rows;
+      const bool split = STREAMS == 2 && rows <= mp.rows;
       if (lane == 0) {
         Item& it = items[n_items % ITEMS];
         it.b = b; it.h = h; it.mt = mt; it.t0 = t0; it.t1 = t1; it.rows = rows; it.klen = klen;
@@ -230,9 +235,9 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         mbar_arrive(&item_full[n_items % ITEMS]);
         if (!end) {
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
+          for (int s = 0; s < STREAMS; ++s) {
             mbar_expect_tx(&qfull[s][buf], (uint32_t)(mp.rows * 128 * U::HALVES));
-            const int node = (mt * 2 + (split ? 0 : s)) * nodes;
+            const int node = (mt * STREAMS + (split ? 0 : s)) * nodes;
             const uint32_t dst = smem_u32(sQ + (s * 2 + buf) * U::QTILE);
 #pragma unroll
             for (int hf = 0; hf < U::HALVES; ++hf)
@@ -295,9 +300,9 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     for (int i = 0; i < U::SLOTS; ++i)
       if (armed & (1u << i)) drain_wait(&full[i], i < slot ? par : par ^ 1u);
     for (int i = max(0, n_items - 2); i < n_items; ++i)
-      for (int s = 0; s < 2; ++s) drain_wait(&qfull[s][i & 1], (uint32_t)(i >> 1) & 1u);
+      for (int s = 0; s < STREAMS; ++s) drain_wait(&qfull[s][i & 1], (uint32_t)(i >> 1) & 1u);
   } else if (warp <= 2) {
-    if (lane == 0) {
+    if (lane == 0 && warp <= STREAMS) {
       // ---------------- products of stream s ----------------
       constexpr uint32_t BASE = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 4) << 24);
       constexpr uint32_t ID_QK = BASE | ((uint32_t)(UBK >> 3) << 17);
@@ -403,23 +408,23 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const uint32_t par = (uint32_t)(i >> 1) & 1u;
         bool got = true;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < STREAMS; ++s) {
           got = got && wait_bar(&staged[s][buf], par, abort_flag, err);
           // both streams of a split item stage in stream 0's buffer
-          const int first = (w.mt * 2 + s) * nodes;
+          const int first = (w.mt * STREAMS + s) * nodes;
           if (got && w.whole && (w.split ? s == 1 : first < p.n)) {
             const uint32_t src = smem_u32(sQ + ((w.split ? 0 : s) * 2 + buf) * U::QTILE);
 #pragma unroll
             for (int hf = 0; hf < U::HALVES; ++hf)
-              tma_store_4d(&tmO, src + hf * U::QHALF, hf * 64, w.h * p.g,
+              if (hf * 64 < p.d) tma_store_4d(&tmO, src + hf * U::QHALF, hf * 64, w.h * p.g,
                            w.split ? w.mt * 2 * nodes : first, w.b);
           }
         }
         if (!got) break;
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        mbar_arrive(&qempty[0][buf]);
-        mbar_arrive(&qempty[1][buf]);
+#pragma unroll
+        for (int s = 0; s < STREAMS; ++s) mbar_arrive(&qempty[s][buf]);
       }
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
@@ -442,7 +447,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       mbar_arrive(&pair);
       (void)wait(&pair, met++ & 1u);
     };
-    for (;; ++n_items) {
+    for (; s < STREAMS; ++n_items) {
       const int slot_i = n_items % ITEMS, buf = n_items & 1;
       if (!wait(&item_full[slot_i], (uint32_t)(n_items / ITEMS) & 1u)) break;
       const Item& w = items[slot_i];
@@ -566,7 +571,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       // (a stream without tiles has not seen its queries arrive)
       (void)wait(&qfull[s][buf], (uint32_t)(n_items >> 1) & 1u);
       float row_m = ms, row_l = l;
-      if (!split) {
+      if (STREAMS == 1 || !split) {
         const float f = whole ? inverse(l) : 1.f;
 #pragma unroll
         for (int j = 0; j < DP / 64; ++j) {
@@ -645,8 +650,9 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 }
 
 // Joins the pieces of the split item that block blockIdx.x began: a thread a row and
-// two 4-column groups (blockIdx.y: 8 groups of 32 rows x 4 of columns; one request of 64
+// NC 4-column groups, 16 apart (blockIdx.y: 8 groups of 32 rows x 4 of columns; one request of 64
 // nodes over 8000 tokens takes 46, 41, 37 and 42 us with 1, 2, 4 and 8 of columns).
+template <int NC>
 __global__ void __launch_bounds__(128) attn_umma_join_kernel(AttnParams p, int rows_tile) {
   pdl_wait();
   pdl_trigger();
@@ -656,39 +662,41 @@ __global__ void __launch_bounds__(128) attn_umma_join_kernel(AttnParams p, int r
   if (m.x < 0) return;
   const int b = m.x, h = m.y & 1023, rows = m.y >> 10, mt = m.z, slot = m.w & 1, last = m.w >> 1;
   const int place = (blockIdx.y >> 2) * 32 + (threadIdx.x & 31);
-  const int w = (blockIdx.y & 3) * 4 + (threadIdx.x >> 5);       // column groups w, w + 16
+  const int w = (blockIdx.y & 3) * 4 + (threadIdx.x >> 5);       // column groups w, w + 16, ..
   const int s = place >> 7, rr = place & 127;
   const int d4 = p.d / 4;
   if (rr >= rows_tile || s * rows_tile + rr >= rows || w >= d4) return;
   JoinState st;
   st.begin();
-  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  const int w1 = w + 16 < d4 ? w + 16 : w;
-  for (int k0 = c; k0 <= last; k0 += JOIN_AHEAD) {
-    float2 a[JOIN_AHEAD];
-    float4 x[JOIN_AHEAD], y[JOIN_AHEAD];
+  float4 acc[NC];
 #pragma unroll
-    for (int j = 0; j < JOIN_AHEAD; ++j) {
+  for (int i = 0; i < NC; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int AHEAD = JOIN_AHEAD * 2 / NC;
+  for (int k0 = c; k0 <= last; k0 += AHEAD) {
+    float2 a[AHEAD];
+    float4 x[AHEAD][NC];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
       const int k = min(k0 + j, last);
       const long long at = (long long)k * 2 + (k == c ? slot : 0);
       const float4* po = reinterpret_cast<const float4*>(p.po) + at * d4 * UROWS + place;
       a[j] = p.pml[at * UROWS + place];
-      x[j] = po[w * UROWS];
-      y[j] = po[w1 * UROWS];
+#pragma unroll
+      for (int i = 0; i < NC; ++i) x[j][i] = po[(w + 16 * i < d4 ? w + 16 * i : w) * UROWS];
     }
 #pragma unroll
-    for (int j = 0; j < JOIN_AHEAD; ++j) {
+    for (int j = 0; j < AHEAD; ++j) {
       if (k0 + j > last) break;
       const float2 f = st.add(a[j]);
-      join_add(acc[0], x[j], f);
-      join_add(acc[1], y[j], f);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) join_add(acc[i], x[j][i], f);
     }
   }
   const int row = mt * p.bm + s * rows_tile + rr, node = row / p.g;
   const long long o = ((long long)b * p.n + node) * p.hq + h * p.g + (row - node * p.g);
   const float inv = inverse(st.l);
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
+  for (int j = 0; j < NC; ++j)
     if (w + 16 * j < d4)
       store_out(static_cast<__nv_bfloat16*>(p.out) + o * p.d + (w + 16 * j) * 4,
                 make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv));
@@ -750,7 +758,7 @@ cudaError_t run_umma(const AttnParams& p, const CUtensorMap& q, const CUtensorMa
   }
   if (e != cudaSuccess) return e;
   TraceScope t(s, "attn_umma_join");
-  return launch_pdl(attn_umma_join_kernel, dim3(grid, UROWS / 32 * 4), dim3(128), 0, s, 1, p, mp.rows);
+  return launch_pdl(attn_umma_join_kernel<DP == 256 ? 4 : 2>, dim3(grid, UROWS / 32 * 4), dim3(128), 0, s, 1, p, mp.rows);
 }
 
 }  // namespace
@@ -772,7 +780,7 @@ cudaError_t launch_attn_umma(AttnParams p, int grid, cudaStream_t s) {
   while ((1 << mp.shift) < rows) ++mp.shift;
   const int nodes = 128 / p.g;
   mp.rows = nodes * p.g;
-  p.bm = 2 * mp.rows;
+  p.bm = (p.d > 128 ? 1 : 2) * mp.rows;
   // costs fitted to the cycles of 148 blocks over mixed items
   p.half = mp.rows;
   p.many = 4;
@@ -783,8 +791,9 @@ cudaError_t launch_attn_umma(AttnParams p, int grid, cudaStream_t s) {
       !encode_rows(&o, p.out, p, row * p.n, row, p.d, nodes) || !encode_cache(&k, p.k, p, rows, &mp.slot_dim) ||
       !encode_cache(&v, p.v, p, rows, &mp.slot_dim))
     return cudaErrorNotSupported;
-  return p.d <= 64 ? run_umma<64>(p, q, k, v, o, mp, grid, s)
-                  : run_umma<128>(p, q, k, v, o, mp, grid, s);
+  if (p.d <= 64) return run_umma<64>(p, q, k, v, o, mp, grid, s);
+  if (p.d <= 128) return run_umma<128>(p, q, k, v, o, mp, grid, s);
+  return run_umma<256>(p, q, k, v, o, mp, grid, s);
 }
 
 }  // namespace pct

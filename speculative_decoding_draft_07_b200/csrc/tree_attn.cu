@@ -34,7 +34,7 @@ AttnPlan plan(const kv_cache_desc& kv, int batch, int n, int hq) {
   // The tcgen05 kernel from 33 rows on (32 requests of 500 to 32768 tokens, 8 heads of
   // 128: 64 rows take 765 us on the warp-level kernel and 440 us on this one, 32 rows
   // 369 us there), where its tiles can hold the rows and the pages.
-  P.umma = kv.dtype == PCT_BF16 && rows > 32 && kv.head_dim <= 128 && attn_umma_pages(kv.page_size);
+  P.umma = kv.dtype == PCT_BF16 && rows > 32 && attn_umma_pages(kv.page_size);
   P.bm = attn_mma_rows((int)std::min<long long>(rows, 1 << 20));
   P.grid = num_sms() * (kv.dtype == PCT_BF16 ? attn_mma_blocks(kv.head_dim)
                                              : attn_f32_blocks(kv.head_dim));

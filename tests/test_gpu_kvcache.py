@@ -122,6 +122,8 @@ SHAPES = [
     dict(n=9, ctx=(8, 30, 64, 0), counts=[9, 0, 1, 4]), dict(n=70, ctx=(513, 127, 0), counts=[70, 3, 64], hq=8, hkv=2, d=128, page=128),
     dict(n=3, ctx=(60,), hq=64, hkv=1, d=64), dict(n=5, ctx=(90, 0), hq=48, hkv=1, d=128),
     dict(n=400, ctx=(150, 0), hq=2, hkv=1, d=64, mask=None), dict(n=50, ctx=(200, 3), hq=2, hkv=2, d=112, page=8),
+    dict(n=70, ctx=(300, 5), hq=4, hkv=2, d=200), dict(n=40, ctx=(64, 700), hq=3, hkv=1, d=136, page=40),
+    dict(n=300, ctx=(0, 20), hq=2, hkv=1, d=256, page=64, mask=None),
 ]
 
 
