@@ -50,7 +50,7 @@ constexpr int UBK = 64;                  // tokens of a key tile
 constexpr int UTHREADS = 384;
 constexpr int UROWS = 256;               // row places of a piece (two streams of 128)
 constexpr int GONE = 8;                  // tiles whose bad-page marks are kept
-constexpr int ITEMS = 4;                 // published items
+constexpr int ITEMS = 8;                 // published items
 
 template <int DP> struct UShape {
   static constexpr int STREAMS = DP == 256 ? 1 : 2;        // (two accumulators fill tensor memory)
@@ -125,8 +125,10 @@ __device__ __forceinline__ void fence_async_smem() {
 
 // An item as the producer publishes it. seq numbers the key tiles that the block
 // loads (their ring slots follow from it). The producer publishes item i only when
-// both softmax groups are done with item i - 2 (their query buffers are free), so
-// ITEMS entries need no hand-back.
+// both softmax groups are done with item i - 2 (their query buffers are free), and
+// loads no tile further than the ring's SLOTS / 2 past one that an issuer has not
+// handed back. An item has a tile at least, and each issuer passes every tile of it, so
+// no entry of ITEMS is written while a role still has to read it.
 struct Item {
   int b, h, mt, t0, t1, rows, klen, ctx, seq;
   int last;                              // no more items; the rest is not set
@@ -148,6 +150,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                  const AttnParams p, const UMaps mp) {
   typedef UShape<DP> U;
   constexpr int STREAMS = U::STREAMS;
+  static_assert(U::SLOTS / 2 < ITEMS && U::SLOTS / 2 < GONE, "entries outlive the ring's tiles");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sQ = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));   // [stream][2]
@@ -311,9 +314,13 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const uint64_t q_desc = make_desc(smem_u32(sQ + s * 2 * U::QTILE), 16, 1024);
       const uint64_t k_desc = make_desc(smem_u32(ring), 16, 1024);
       const uint64_t v_desc = make_desc(smem_u32(ring), U::KHALF, 1024);
-      // the item in hand, its next tile for S and its end; S and P V issued
-      int item = -1, t = 0, t1 = 0, seq = 0, step = 1, n_s = 0, n_pv = 0;
-      // per score buffer, of the P V to come: V's ring position << 2 | split << 1 | first
+      // Every issuer waits for every fill of every ring slot and hands it back, also
+      // for the other stream's tiles of a split item: a parity tells a fill from the one
+      // before only to a reader that has seen the one before arrive.
+      // The item in hand, its next tile and its end, the first of this stream; S and
+      // P V issued
+      int item = -1, t = 0, t1 = 0, mine = 0, seq = 0, step = 1, n_s = 0, n_pv = 0;
+      // per score buffer, of the P V to come: V's ring position << 1 | first
       int todo0 = 0, todo1 = 0;
       bool head = true, live = true;
       long long c0 = 0;
@@ -324,7 +331,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         bool moved = false;
         if (n_pv < n_s) {
           const int bf = n_pv & 1, td = bf ? todo1 : todo0;
-          const int pos = td >> 2, slot = pos % U::SLOTS;
+          const int pos = td >> 1, slot = pos % U::SLOTS;
           if (mbar_test(&pready[s][bf], (uint32_t)(n_pv >> 1) & 1u) &&
               mbar_test(&full[slot], (uint32_t)(pos / U::SLOTS) & 1u)) {
             tc_fence_after();
@@ -336,7 +343,6 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                       ID_PV, more | (k > 0));
             umma_commit(&pvdone[s][bf]);
             umma_commit(&empty[slot]);
-            if (td & 2) umma_commit(&empty[slot]);      // the other stream does not use it
             ++n_pv;
             moved = true;
           }
@@ -349,12 +355,25 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             if (it.last) {
               live = false;
             } else {
-              t = it.start(s);
+              t = it.t0;
               t1 = it.t1;
+              mine = it.start(s);
               step = it.step();
               seq = it.seq - it.t0;
               head = true;
             }
+            moved = true;
+          }
+        } else if (live && step == 2 && ((t ^ mine) & 1)) {   // the other stream's tile
+          const int pos = (seq + t) * 2, ks = pos % U::SLOTS, vs = (pos + 1) % U::SLOTS;
+          // (of a V tile that this stream has still to multiply, the slot's next fill
+          // cannot be told yet)
+          const bool seen = n_pv == n_s || (((n_pv & 1) ? todo1 : todo0) >> 1) + U::SLOTS > pos + 1;
+          if (seen && mbar_test(&full[ks], (uint32_t)(pos / U::SLOTS) & 1u) &&
+              mbar_test(&full[vs], (uint32_t)((pos + 1) / U::SLOTS) & 1u)) {
+            mbar_arrive(&empty[ks]);
+            mbar_arrive(&empty[vs]);
+            ++t;
             moved = true;
           }
         } else if (live && n_s - n_pv < 2) {
@@ -372,12 +391,11 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                        kd + (uint64_t)(((k >> 2) * U::KHALF + (k & 3) * 32) >> 4), ID_QK, k > 0);
             umma_commit(&sfull[s][bf]);
             umma_commit(&empty[slot]);
-            if (step == 2) umma_commit(&empty[slot]);
-            const int td = (pos + 1) << 2 | (step == 2) << 1 | (head ? 1 : 0);
+            const int td = (pos + 1) << 1 | (head ? 1 : 0);
             if (bf) todo1 = td; else todo0 = td;
             ++n_s;
             head = false;
-            t += step;
+            ++t;
             moved = true;
           }
         }
@@ -529,7 +547,10 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         l += sum.x + sum.y;
         const int end = klen - k0;                       // tokens of the tile that exist
         if (end < UBK || lost) {
-          // V rows that stand for no token: zero, so that 0 * V is 0
+          // V rows that stand for no token: zero, so that 0 * V is 0. (The fill before
+          // this one in the slot has arrived: it was multiplied at the latest with
+          // this stream's tile before, or handed back before this tile's S.)
+          if (n > 0) (void)wait(&pvdone[s][bf ^ 1], (uint32_t)((n - 1) >> 1) & 1u);
           const int pos = seq * 2 + 1, slot = pos % U::SLOTS;
           (void)wait(&full[slot], (uint32_t)(pos / U::SLOTS) & 1u);
           if (tl < UBK && (tl >= end || (((tl < 32 ? gq.x : gq.y) >> (tl & 31)) & 1u))) {

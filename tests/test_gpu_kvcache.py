@@ -267,6 +267,29 @@ def test_results_repeat_and_do_not_depend_on_the_workspace(dtype, n, hq, batch):
     _check(a, *c) if batch < 100 else None
 
 
+@pytest.mark.parametrize("d,longest", [(96, 63), (64, 63), (128, 400), (64, 700), (200, 63)])
+def test_many_short_items_of_both_kinds(d, longest):
+    """A block's share mixes row tiles with one and with two halves, of one key tile and of several,
+    so that a tile's place in the load ring passes between readers that do and do not use it."""
+    rng = np.random.default_rng(d + longest)
+    B, n, page = 64, 257, 192
+    ctx = [int(x) for x in rng.integers(0, longest + 1, B)]
+    counts = [int(rng.choice([n, 0, 1, rng.integers(0, n + 1), rng.integers(0, 40)])) for _ in range(B)]
+    g, table, _, _, _ = _case(21, hq=32, hkv=8, d=d, page=page, n=n, ctx=ctx, counts=counts, mask=None)
+    first = _run(g)
+    torch.cuda.synchronize()
+    assert not host(first.status).any()
+    want, wl = first.out.clone(), first.lse.clone()
+    for _ in range(20):
+        r = _run(g)
+        torch.cuda.synchronize()
+        assert torch.equal(r.out, want) and torch.equal(r.lse, wl) and not host(r.status).any()
+    for b in range(0, B, 9):
+        one = g | {"q": g["q"][b:b + 1], "ctx": g["ctx"][b:b + 1], "count": g["count"][b:b + 1]}
+        _check(pct.AttnOut(want[b:b + 1], wl[b:b + 1], first.status[b:b + 1]), one, table[b:b + 1],
+               ctx[b:b + 1], counts[b:b + 1], None)
+
+
 def test_many_requests_one_token():
     rng = np.random.default_rng(4)
     c = _case(12, n=1, hq=4, hkv=2, ctx=[int(x) for x in rng.integers(0, 90, 400)], mask=None, page=8)
