@@ -515,6 +515,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           // every product of this stream before P V of this tile is complete
           (void)wait(&pvdone[s][bf ^ 1], (uint32_t)((n - 1) >> 1) & 1u);
           tc_fence_after();
+          __syncwarp();
 #pragma unroll
           for (int j = 0; j < DP / 16; ++j) {
             uint32_t o[16];
@@ -529,6 +530,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const float ref = m == neg_inf() ? 0.f : m * c;
         float2 sum = make_float2(0.f, 0.f);
         const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
+        __syncwarp();                                    // the stores take a converged warp
         // the weights become bf16 (off by at most 2^-8 each, the product's operand
         // type); the sum is that of the fp32 values
 #pragma unroll
@@ -563,6 +565,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           }
           fence_async_smem();
         }
+        __syncwarp();
         tmem_store_wait();
         tc_fence_before();
         mbar_arrive(&pready[s][bf]);
