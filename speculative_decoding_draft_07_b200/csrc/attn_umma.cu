@@ -30,8 +30,8 @@
 // seldom do; weights up to 2^8 lose nothing in fp32 sums and bf16 products.
 // 64 tokens a tile rather than 128: with 128 the scores fill tensor memory once
 // (head_dim 128), so that S, softmax and P V of a stream run one after another
-// (64 requests x 256 nodes over up to 4096 tokens: 1.41 ms; this takes 0.81-0.88,
-// 630-680 TFLOP/s). A 64-token tile of both streams takes about 2000 cycles, 1270 of
+// (64 requests x 256 nodes over up to 4096 tokens: 1.41 ms; this takes 0.77-0.88,
+// 630-720 TFLOP/s). A 64-token tile of both streams takes about 2000 cycles, 1270 of
 // products alone and 1024 of exponentials, which overlap in part.
 // Every mbarrier wait is bounded; when one gives up, the roles run to the end
 // without waiting, drain their copies and products, free the tensor memory, and
