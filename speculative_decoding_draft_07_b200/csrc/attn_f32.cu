@@ -15,6 +15,8 @@
 // the scalar loads of V (two neighbouring keys x 8 columns) find no bank conflicts. The
 // weights' matrix layout pairs keys 2t and 2t + 1 where the next product wants t and
 // t + 4; the order of keys in a sum is free, so V is read in the weights' order.
+#include <type_traits>
+
 #include "attn_warp.cuh"
 
 namespace pct {
@@ -31,7 +33,9 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // x as hi (TF32, to nearest) + lo (the rest; the product reads its upper 19 bits). An
-// infinite x gives lo = NaN: the scores' caller looks for that.
+// infinite x gives lo = NaN, and a finite |x| from 0x7f7ff000 (3.402e38) on is rounded up
+// to hi = inf, lo = -inf; both make every product NaN. The callers look for NaN and take
+// such scores and sums again.
 struct Part { uint32_t hi, lo; };
 __device__ __forceinline__ Part split(uint32_t x) {
   Part p;
@@ -52,6 +56,29 @@ __device__ __forceinline__ void mma_f32(float (&c)[4], float (&e)[4], const Part
   mma_tf32(e, a.lo, b0.hi, b1.hi);
   mma_tf32(e, a.hi, b0.lo, b1.lo);
   mma_tf32(c, a.hi, b0.hi, b1.hi);
+}
+
+// The product of weights a >= 0 with any values b: hi of a very large one is cut off where
+// rounding would make it infinite, and an infinity is hi alone, which only a's hi meets (a's
+// lo may be 0 or negative). Other values come out as by split and mma_f32, bit for bit.
+struct PartB { Part p; uint32_t lo_hi; };              // lo_hi: hi as a's lo meets it
+__device__ __forceinline__ PartB split_any(uint32_t x) {
+  const uint32_t mag = x & 0x7fffffffu;
+  PartB r;
+  r.p = split(x);
+  if (mag >= 0x7f7ff000u && mag <= 0x7f800000u) {
+    r.p.hi = mag == 0x7f800000u ? x : x & 0xffffe000u;
+    r.p.lo = mag == 0x7f800000u ? 0u
+                                : __float_as_uint(__uint_as_float(x) - __uint_as_float(r.p.hi));
+  }
+  r.lo_hi = mag == 0x7f800000u ? 0u : r.p.hi;
+  return r;
+}
+__device__ __forceinline__ void mma_any(float (&c)[4], const PartA& a, const PartB& b0,
+                                        const PartB& b1) {
+  mma_tf32(c, a.lo, b0.lo_hi, b1.lo_hi);
+  mma_tf32(c, a.hi, b0.p.lo, b1.p.lo);
+  mma_tf32(c, a.hi, b0.p.hi, b1.p.hi);
 }
 
 template <int DP, int WM> struct F32Shape {
@@ -137,196 +164,215 @@ __global__ void __launch_bounds__(kF32Threads, F32Shape<DP, WM>::MINB) attn_f32_
       }
     };
 
-    __syncthreads();                                   // the last item's buffers are free
-#pragma unroll
-    for (int i = 0; i < STAGES; ++i)
-      if (t0 + i < t1) find_tile(t0 + i);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < BM * CH / NT; ++i) {
-      const int rr = (i * NT + tid) / CH, c = tid % CH;
-      const float* src = static_cast<const float*>(p.q);
-      int bytes = 0;
-      if (rr < rows && c * 4 < p.d) {
-        const int row = row0 + rr, node = row / p.g, qh = h * p.g + (row - node * p.g);
-        src += b * p.qs_b + node * p.qs_n + qh * p.qs_h + c * 4;
-        bytes = 16;
-      }
-      cp16(sm_addr(Qs) + rr * RB + c * 16, src, bytes);
-    }
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) {
-      if (t0 + i < t1) load_tile(t0 + i);
-      cp_commit();
-    }
-    // this thread's rows and their nodes
     const int ra = wm * 16 + (lane >> 2);
-    int node[2];
-    const uint32_t* words[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int rr = ra + i * 8;
-      node[i] = rr < rows ? (row0 + rr) / p.g : -0x40000000;
-      words[i] = p.mask && rr < rows ? p.mask + ((long long)b * p.n + node[i]) * p.words : nullptr;
-    }
     const uint32_t qa = sm_addr(Qs) + (wm * 16 + (lane & 15)) * RB + (lane >> 4) * 16;
     float acc[DP / 8][4], m[2], l[2];
+    // The item's tiles; whether a sum of P V came out NaN although its row's scores did not.
+    // That is an infinite or very large V: the item is gone through again with mma_any, and
+    // what was not NaN stays as it was. (Two copies of the loop: a call or a branch to the
+    // other products inside one made fp32 decode 40% slower, this one leaves it as it was and
+    // 32 nodes x 4 requests 0.8 of 27 us slower.)
+    auto tiles = [&](auto again) -> bool {
+      __syncthreads();                                   // the last item's buffers are free
 #pragma unroll
-    for (int i = 0; i < DP / 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-    m[0] = m[1] = neg_inf();
-    l[0] = l[1] = 0.f;
-
-    for (int t = t0; t < t1; ++t) {
-      cp_wait<STAGES - 2>();
+      for (int i = 0; i < STAGES; ++i)
+        if (t0 + i < t1) find_tile(t0 + i);
       __syncthreads();
-      if (t + STAGES - 1 < t1) load_tile(t + STAGES - 1);
-      cp_commit();
-      if (t + STAGES < t1) find_tile(t + STAGES);
-      const int st = (t - t0) % STAGES;
-      const uint32_t kd = sm_addr(ring + st * 2 * TILE);
-      const uint32_t* Vs = reinterpret_cast<const uint32_t*>(ring + (st * 2 + 1) * TILE);
-      // few keys a warp: more accumulators, so that products do not wait for each other
-      constexpr int E = KW <= 16 ? 2 : 1;
-      float s[KW / 8][4], s2[KW / 8][4], e[KW / 8][E][4];
 #pragma unroll
-      for (int i = 0; i < KW / 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j] = e[i][0][j] = e[i][E - 1][j] = 0.f;
-#pragma unroll
-      for (int k = 0; k < DP / 16; ++k) {              // 16 columns: two steps of 8
-        PartA a[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t x[4];
-          ldsm4(qa + (2 * k + q) * 32, x);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) a[q].set(j, x[j]);
+      for (int i = 0; i < BM * CH / NT; ++i) {
+        const int rr = (i * NT + tid) / CH, c = tid % CH;
+        const float* src = static_cast<const float*>(p.q);
+        int bytes = 0;
+        if (rr < rows && c * 4 < p.d) {
+          const int row = row0 + rr, node = row / p.g, qh = h * p.g + (row - node * p.g);
+          src += b * p.qs_b + node * p.qs_n + qh * p.qs_h + c * 4;
+          bytes = 16;
         }
-#pragma unroll
-        for (int i = 0; i < KW / 8; ++i) {
-          uint32_t x[4];                               // columns 0-3, 4-7, 8-11, 12-15 of 8 keys
-          ldsm4(kd + (wk * KW + i * 8 + (lane & 7)) * RB + k * 64 + (lane >> 3) * 16, x);
-          mma_f32(s[i], e[i][0], a[0], split(x[0]), split(x[1]));
-          mma_f32(s2[i], e[i][E - 1], a[1], split(x[2]), split(x[3]));
-        }
+        cp16(sm_addr(Qs) + rr * RB + c * 16, src, bytes);
       }
 #pragma unroll
-      for (int i = 0; i < KW / 8; ++i)
+      for (int i = 0; i < STAGES - 1; ++i) {
+        if (t0 + i < t1) load_tile(t0 + i);
+        cp_commit();
+      }
+      // this thread's rows and their nodes
+      int node[2];
+      const uint32_t* words[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          s[i][j] = (s[i][j] + s2[i][j]) + (E == 2 ? e[i][0][j] + e[i][E - 1][j] : e[i][0][j]);
-      // An infinite key (or query) makes NaN of the parts where the score may be
-      // infinite: such a tile's scores are taken again as plain sums. (Rare.)
-      bool bad = false;
+      for (int i = 0; i < 2; ++i) {
+        const int rr = ra + i * 8;
+        node[i] = rr < rows ? (row0 + rr) / p.g : -0x40000000;
+        words[i] = p.mask && rr < rows ? p.mask + ((long long)b * p.n + node[i]) * p.words : nullptr;
+      }
 #pragma unroll
-      for (int i = 0; i < KW / 8; ++i)
+      for (int i = 0; i < DP / 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) bad |= !(s[i][j] == s[i][j]);
-      if (__any_sync(0xffffffffu, bad)) {
-        const float* Kf = reinterpret_cast<const float*>(ring + st * 2 * TILE);
-        const float* Qf = reinterpret_cast<const float*>(Qs);
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+      m[0] = m[1] = neg_inf();
+      l[0] = l[1] = 0.f;
+
+      for (int t = t0; t < t1; ++t) {
+        cp_wait<STAGES - 2>();
+        __syncthreads();
+        if (t + STAGES - 1 < t1) load_tile(t + STAGES - 1);
+        cp_commit();
+        if (t + STAGES < t1) find_tile(t + STAGES);
+        const int st = (t - t0) % STAGES;
+        const uint32_t kd = sm_addr(ring + st * 2 * TILE);
+        const uint32_t* Vs = reinterpret_cast<const uint32_t*>(ring + (st * 2 + 1) * TILE);
+        // few keys a warp: more accumulators, so that products do not wait for each other
+        constexpr int E = KW <= 16 ? 2 : 1;
+        float s[KW / 8][4], s2[KW / 8][4], e[KW / 8][E][4];
 #pragma unroll
         for (int i = 0; i < KW / 8; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float* kr = Kf + (wk * KW + i * 8 + 2 * (lane & 3) + (j & 1)) * (RB / 4);
-            const float* qr = Qf + (ra + (j >> 1) * 8) * (RB / 4);
-            float x = 0.f;
-            for (int d = 0; d < p.d; ++d) x = fmaf(qr[d], kr[d], x);
-            s[i][j] = x;
+          for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j] = e[i][0][j] = e[i][E - 1][j] = 0.f;
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {              // 16 columns: two steps of 8
+          PartA a[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t x[4];
+            ldsm4(qa + (2 * k + q) * 32, x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[q].set(j, x[j]);
           }
-      }
 #pragma unroll
-      for (int i = 0; i < KW / 8; ++i)
+          for (int i = 0; i < KW / 8; ++i) {
+            uint32_t x[4];                               // columns 0-3, 4-7, 8-11, 12-15 of 8 keys
+            ldsm4(kd + (wk * KW + i * 8 + (lane & 7)) * RB + k * 64 + (lane >> 3) * 16, x);
+            mma_f32(s[i], e[i][0], a[0], split(x[0]), split(x[1]));
+            mma_f32(s2[i], e[i][E - 1], a[1], split(x[2]), split(x[3]));
+          }
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[i][j] *= p.scale_log2;
-      const int key0 = t * BK + wk * KW;               // the warp's first token
-      const unsigned long long lost = gone[t & 3];
-      if (key0 + KW > ctx || lost) {                   // nodes, the end, or a bad page
+        for (int i = 0; i < KW / 8; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+          for (int j = 0; j < 4; ++j)
+            s[i][j] = (s[i][j] + s2[i][j]) + (E == 2 ? e[i][0][j] + e[i][E - 1][j] : e[i][0][j]);
+        // An infinite key (or query) makes NaN of the parts where the score may be
+        // infinite: such a tile's scores are taken again as plain sums. (Rare.)
+        bool bad = false;
 #pragma unroll
-          for (int w = 0; w < (KW + 31) / 32; ++w) {
-            uint32_t bits = seen32(p, words[i], node[i], key0 + w * 32 - ctx);
-            bits &= ~(uint32_t)(lost >> (wk * KW + w * 32));
+        for (int i = 0; i < KW / 8; ++i)
 #pragma unroll
-            for (int j = 0; j < 4 && w * 4 + j < KW / 8; ++j) {
-              const uint32_t two = bits >> (j * 8 + 2 * (lane & 3));
-              if (!(two & 1u)) s[w * 4 + j][2 * i] = neg_inf();
-              if (!(two & 2u)) s[w * 4 + j][2 * i + 1] = neg_inf();
+          for (int j = 0; j < 4; ++j) bad |= !(s[i][j] == s[i][j]);
+        if (__any_sync(0xffffffffu, bad)) {
+          const float* Kf = reinterpret_cast<const float*>(ring + st * 2 * TILE);
+          const float* Qf = reinterpret_cast<const float*>(Qs);
+#pragma unroll
+          for (int i = 0; i < KW / 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float* kr = Kf + (wk * KW + i * 8 + 2 * (lane & 3) + (j & 1)) * (RB / 4);
+              const float* qr = Qf + (ra + (j >> 1) * 8) * (RB / 4);
+              float x = 0.f;
+              for (int d = 0; d < p.d; ++d) x = fmaf(qr[d], kr[d], x);
+              s[i][j] = x;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < KW / 8; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[i][j] *= p.scale_log2;
+        const int key0 = t * BK + wk * KW;               // the warp's first token
+        const unsigned long long lost = gone[t & 3];
+        if (key0 + KW > ctx || lost) {                   // nodes, the end, or a bad page
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int w = 0; w < (KW + 31) / 32; ++w) {
+              uint32_t bits = seen32(p, words[i], node[i], key0 + w * 32 - ctx);
+              bits &= ~(uint32_t)(lost >> (wk * KW + w * 32));
+#pragma unroll
+              for (int j = 0; j < 4 && w * 4 + j < KW / 8; ++j) {
+                const uint32_t two = bits >> (j * 8 + 2 * (lane & 3));
+                if (!(two & 1u)) s[w * 4 + j][2 * i] = neg_inf();
+                if (!(two & 2u)) s[w * 4 + j][2 * i + 1] = neg_inf();
+              }
             }
           }
         }
-      }
-      float mn[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float x = s[0][2 * i];
-#pragma unroll
-        for (int j = 0; j < KW / 8; ++j) x = fmaxf(x, fmaxf(s[j][2 * i], s[j][2 * i + 1]));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        mn[i] = fmaxf(m[i], x);
-      }
-      if (__any_sync(0xffffffffu, mn[0] != m[0] || mn[1] != m[1])) {
+        float mn[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float f = mn[i] == neg_inf() ? 1.f : ex2(m[i] - mn[i]);
-          l[i] *= f;
-          m[i] = mn[i];
+          float x = s[0][2 * i];
 #pragma unroll
-          for (int j = 0; j < DP / 8; ++j) {
-            acc[j][2 * i] *= f;
-            acc[j][2 * i + 1] *= f;
+          for (int j = 0; j < KW / 8; ++j) x = fmaxf(x, fmaxf(s[j][2 * i], s[j][2 * i + 1]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          mn[i] = fmaxf(m[i], x);
+        }
+        if (__any_sync(0xffffffffu, mn[0] != m[0] || mn[1] != m[1])) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float f = mn[i] == neg_inf() ? 1.f : ex2(m[i] - mn[i]);
+            l[i] *= f;
+            m[i] = mn[i];
+#pragma unroll
+            for (int j = 0; j < DP / 8; ++j) {
+              acc[j][2 * i] *= f;
+              acc[j][2 * i + 1] *= f;
+            }
           }
         }
-      }
-      const float ref[2] = {m[0] == neg_inf() ? 0.f : m[0], m[1] == neg_inf() ? 0.f : m[1]};
+        const float ref[2] = {m[0] == neg_inf() ? 0.f : m[0], m[1] == neg_inf() ? 0.f : m[1]};
 #pragma unroll
-      for (int j = 0; j < KW / 8; ++j)
+        for (int j = 0; j < KW / 8; ++j)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          s[j][2 * i] = ex2(s[j][2 * i] - ref[i]);
-          s[j][2 * i + 1] = ex2(s[j][2 * i + 1] - ref[i]);
-          l[i] += s[j][2 * i] + s[j][2 * i + 1];
+          for (int i = 0; i < 2; ++i) {
+            s[j][2 * i] = ex2(s[j][2 * i] - ref[i]);
+            s[j][2 * i + 1] = ex2(s[j][2 * i + 1] - ref[i]);
+            l[i] += s[j][2 * i] + s[j][2 * i + 1];
+          }
+        // A tile's sum of P V is begun afresh and added to the accumulator by an fp32 add:
+        // the matrix unit cuts its sums off instead of rounding them, which over a long
+        // chain of tiles would add up to one side.
+        PartA a[KW / 8];                                 // keys 2t and 2t + 1 of each eight
+#pragma unroll
+        for (int i = 0; i < KW / 8; ++i) {
+          a[i].set(0, __float_as_uint(s[i][0]));
+          a[i].set(1, __float_as_uint(s[i][2]));
+          a[i].set(2, __float_as_uint(s[i][1]));
+          a[i].set(3, __float_as_uint(s[i][3]));
         }
-      // A tile's sum of P V is begun afresh and added to the accumulator by an fp32 add:
-      // the matrix unit cuts its sums off instead of rounding them, which over a long
-      // chain of tiles would add up to one side.
-      PartA a[KW / 8];                                 // keys 2t and 2t + 1 of each eight
+        const uint32_t* vr = Vs + (wk * KW + 2 * (lane & 3)) * (RB / 4) + (lane >> 2);
 #pragma unroll
-      for (int i = 0; i < KW / 8; ++i) {
-        a[i].set(0, __float_as_uint(s[i][0]));
-        a[i].set(1, __float_as_uint(s[i][2]));
-        a[i].set(2, __float_as_uint(s[i][1]));
-        a[i].set(3, __float_as_uint(s[i][3]));
+        for (int j = 0; j < DP / 8; ++j) {
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < KW / 8; ++i) {
+            const uint32_t v0 = vr[i * 8 * (RB / 4) + j * 8], v1 = vr[(i * 8 + 1) * (RB / 4) + j * 8];
+            if constexpr (decltype(again)::value) mma_any(c, a[i], split_any(v0), split_any(v1));
+            else mma_f32(c, c, a[i], split(v0), split(v1));
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[j][q] += c[q];
+        }
+        if (lost) {                                      // rare: clear the mark for the stage's next tile
+          __syncthreads();
+          if (tid == 0) gone[t & 3] = 0;
+        }
       }
-      const uint32_t* vr = Vs + (wk * KW + 2 * (lane & 3)) * (RB / 4) + (lane >> 2);
+      cp_wait<0>();
+      bool lost_sum = false;
 #pragma unroll
-      for (int j = 0; j < DP / 8; ++j) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < 2; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        if ((lane & 3) == 0) ml[wk][ra + i * 8] = make_float2(m[i], l[i]);
+        bool nan = false;
 #pragma unroll
-        for (int i = 0; i < KW / 8; ++i)
-          mma_f32(c, c, a[i], split(vr[i * 8 * (RB / 4) + j * 8]),
-                  split(vr[(i * 8 + 1) * (RB / 4) + j * 8]));
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[j][q] += c[q];
+        for (int j = 0; j < DP / 8; ++j)
+          nan |= !(acc[j][2 * i] == acc[j][2 * i]) || !(acc[j][2 * i + 1] == acc[j][2 * i + 1]);
+        lost_sum |= nan && l[i] == l[i];
       }
-      if (lost) {                                      // rare: clear the mark for the stage's next tile
-        __syncthreads();
-        if (tid == 0) gone[t & 3] = 0;
-      }
+      return lost_sum;
+    };
+    if (__syncthreads_or(tiles(std::false_type()))) {
+      tiles(std::true_type());
+      __syncthreads();
     }
-    cp_wait<0>();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if ((lane & 3) == 0) ml[wk][ra + i * 8] = make_float2(m[i], l[i]);
-    }
-    __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float mx = neg_inf();
