@@ -250,8 +250,9 @@ __global__ void __launch_bounds__(kF32Threads, F32Shape<DP, WM>::MINB) attn_f32_
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             s[i][j] = (s[i][j] + s2[i][j]) + (E == 2 ? e[i][0][j] + e[i][E - 1][j] : e[i][0][j]);
-        // An infinite key (or query) makes NaN of the parts where the score may be
-        // infinite: such a tile's scores are taken again as plain sums. (Rare.)
+        // An infinite or very large key (or query) makes NaN of the parts where the score need
+        // not be: scores that are NaN are taken again as plain sums, and only those, so that a
+        // key changes no row that does not see it. (Rare.)
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < KW / 8; ++i)
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kF32Threads, F32Shape<DP, WM>::MINB) attn_f32_
               const float* qr = Qf + (ra + (j >> 1) * 8) * (RB / 4);
               float x = 0.f;
               for (int d = 0; d < p.d; ++d) x = fmaf(qr[d], kr[d], x);
-              s[i][j] = x;
+              s[i][j] = s[i][j] == s[i][j] ? s[i][j] : x;
             }
         }
 #pragma unroll

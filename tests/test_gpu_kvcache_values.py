@@ -73,3 +73,19 @@ def test_the_largest_value_of_an_unseen_node(n, hq, d):
     r = _run(g)
     torch.cuda.synchronize()
     assert torch.equal(r.out, want) and torch.equal(r.lse, wl)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), FMAX])
+@pytest.mark.parametrize("d", [64, 128, 200])
+@pytest.mark.parametrize("n,hq", [(6, 8), (60, 8)])
+def test_fp32_keys_of_unseen_nodes_do_not_enter(n, hq, d, bad):
+    """As test_keys_of_unseen_nodes_do_not_enter, in fp32: no other row's result changes by a bit."""
+    g, table, ctx, counts, m = _case(7, dtype="f32", n=n, hq=hq, d=d, ctx=(33, 100), mask="random")
+    m &= np.uint32(0xfffffffd)
+    g["mask"] = torch.from_numpy(m.view(np.int32)).to(DEV)
+    want, wl = _clean(g)
+    for b in range(2):
+        g["k"][_place(table, b, ctx[b] + 1)] = bad
+    r = _run(g)
+    torch.cuda.synchronize()
+    assert torch.equal(r.out, want) and torch.equal(r.lse, wl)
