@@ -138,6 +138,18 @@ struct Item {
   __device__ int step() const { return split ? 2 : 1; }
 };
 
+// The factor from scores to exponents of a row with maximum m: c, but for |m c| from 2^28 on
+// (infinities too) the power of two that brings |m| into [2^30, 2^31). A weight is
+// 2^(x c - ref) with ref = m c rounded once, so the maximum's own is off by half a step of ref
+// in the exponent: at most 8 below 2^28, past an exponential's range from 2^31 on. With a power
+// of two it is exact. There two scores next to each other differ by 2^4 at least with c and by
+// 2^6 at least with the power of two: the maximum's weight is 1 and any smaller score's nothing.
+__device__ __forceinline__ float row_factor(float m, float c) {
+  if (!(fabsf(m) * c >= 268435456.f) || m == neg_inf()) return c;
+  const uint32_t e = (__float_as_uint(m) >> 23) & 255u;
+  return __uint_as_float(min(284u - e, 254u) << 23);
+}
+
 // One accumulator column pair of 8: 16 bytes of a bf16 row.
 __device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
   return make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
@@ -479,7 +491,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const uint32_t* words =
           p.mask && valid ? p.mask + ((long long)w.b * p.n + node) * p.words : nullptr;
       const int ctx = w.ctx, seq0 = w.seq - w.t0, klen = w.klen, t1 = w.t1, step = w.step();
-      float m = neg_inf(), l = 0.f;
+      float m = neg_inf(), l = 0.f, cr = c;
       const int n0 = n;
       for (int t = w.start(s); t < t1; t += step, ++n) {
         const int seq = seq0 + t, k0 = t * UBK, bf = n & 1;
@@ -526,10 +538,13 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             tmem_store16(aO + j * 16, o);
           }
         }
-        if (move) m = mn;
-        const float ref = m == neg_inf() ? 0.f : m * c;
+        if (move) {
+          m = mn;
+          cr = row_factor(m, c);
+        }
+        const float ref = m == neg_inf() ? 0.f : m * cr;
         float2 sum = make_float2(0.f, 0.f);
-        const float2 c2 = make_float2(c, c), r2 = make_float2(-ref, -ref);
+        const float2 c2 = make_float2(cr, cr), r2 = make_float2(-ref, -ref);
         __syncwarp();                                    // the stores take a converged warp
         // the weights become bf16 (off by at most 2^-8 each, the product's operand
         // type); the sum is that of the fp32 values

@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+from gpu_util import f64
 from test_gpu_kvcache import DEV, _case, _check, _run
 
 pytestmark = pytest.mark.gpu
@@ -89,3 +90,35 @@ def test_fp32_keys_of_unseen_nodes_do_not_enter(n, hq, d, bad):
     r = _run(g)
     torch.cuda.synchronize()
     assert torch.equal(r.out, want) and torch.equal(r.lse, wl)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("n,hq,d", [(1, 8, 64), (60, 2, 64), (60, 8, 128), (60, 2, 200)])
+def test_scores_of_any_size(n, hq, d, sign, dtype):
+    """Scores of 2^32 to 2^40, exact in every format and far apart: a row is its best token's V.
+
+    The best weight is 1 and the others are 0, so bf16 is exact. In fp32, V = hi + lo with hi its 11
+    leading bits to nearest, |lo| <= 2^-11 |v|; the product reads 11 bits of lo, cut off, which leaves
+    out at most 2^-10 |lo| <= 2^-21 |v|, and the sum of the parts, the accumulator's add and the
+    division are off by at most 2^-23 + 2 * 2^-24 = 2^-22 of it: together below 2^-20 |v|."""
+    g, table, ctx, counts, _ = _case(33, dtype=dtype, n=n, hq=hq, hkv=1, d=d, mask=None,
+                                     ctx=(150, 33, 64, 127, 128, 5, 90, 1))
+    g["q"].zero_()
+    g["q"][..., 0] = 2.0 ** 20
+    for b in range(len(ctx)):
+        for t in range(ctx[b] + counts[b]):
+            g["k"][_place(table, b, t)][:, 0] = sign * ((37 * t + 11 * b) % 251 + 1) * 2.0 ** 8
+    r = _run(g, scale=16.0)
+    torch.cuda.synchronize()
+    out, lse = f64(r.out), f64(r.lse)
+    v = f64(g["v"])
+    for b in range(len(ctx)):
+        score = np.array([sign * ((37 * t + 11 * b) % 251 + 1) * 2.0 ** 32 for t in range(ctx[b] + counts[b])])
+        for i in range(n):
+            best = int(score[: ctx[b] + i + 1].argmax())
+            best_v = v[_place(table, b, best)]
+            off = 0 if dtype == "bf16" else 2.0 ** -20
+            assert (np.abs(out[b, i] - best_v) <= off * np.abs(best_v)).all(), (b, i)
+            # base-2 and back: three roundings, and log2 e and ln 2 in fp32
+            assert (np.abs(lse[b, i] - score[best]) <= 2.0 ** -21 * abs(score[best])).all(), (b, i)
