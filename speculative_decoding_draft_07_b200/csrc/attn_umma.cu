@@ -26,8 +26,8 @@
 // and are added up at the item's end (both accumulators sit in the same tensor
 // memory lanes). Tensor memory: S (2 streams x 2 buffers x 64 columns, P in the
 // first 32 of its S), then O_0, O_1. The accumulator is rescaled only when a row's
-// maximum grows by more than 2^8 over the reference in use, which the later tiles
-// seldom do; weights up to 2^8 lose nothing in fp32 sums and bf16 products.
+// maximum grows by more than 2^8 over the one in use, which the later tiles seldom do;
+// weights are taken relative to 2^8 times that one, so none is above 1.
 // 64 tokens a tile rather than 128: with 128 the scores fill tensor memory once
 // (head_dim 128), so that S, softmax and P V of a stream run one after another
 // (64 requests x 256 nodes over up to 4096 tokens: 1.41 ms; this takes 0.77-0.88,
@@ -148,6 +148,13 @@ __device__ __forceinline__ float row_factor(float m, float c) {
   if (!(fabsf(m) * c >= 268435456.f) || m == neg_inf()) return c;
   const uint32_t e = (__float_as_uint(m) >> 23) & 255u;
   return __uint_as_float(min(284u - e, 254u) << 23);
+}
+
+// The reference of a row's weights: 8 above its m, which may be that far behind the running
+// maximum, so that no weight is above 1 and large values overflow no sooner than with the
+// maximum itself. (With row_factor's power of two m is never behind.)
+__device__ __forceinline__ float row_ref(float m, float cr, float c) {
+  return fmaf(m, cr, cr == c ? 8.f : 0.f);
 }
 
 // One accumulator column pair of 8: 16 bytes of a bf16 row.
@@ -491,7 +498,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const uint32_t* words =
           p.mask && valid ? p.mask + ((long long)w.b * p.n + node) * p.words : nullptr;
       const int ctx = w.ctx, seq0 = w.seq - w.t0, klen = w.klen, t1 = w.t1, step = w.step();
-      float m = neg_inf(), l = 0.f, cr = c;
+      float m = neg_inf(), l = 0.f, cr = c, ref = 0.f;
       const int n0 = n;
       for (int t = w.start(s); t < t1; t += step, ++n) {
         const int seq = seq0 + t, k0 = t * UBK, bf = n & 1;
@@ -541,8 +548,8 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (move) {
           m = mn;
           cr = row_factor(m, c);
+          ref = row_ref(m, cr, c);
         }
-        const float ref = m == neg_inf() ? 0.f : m * cr;
         float2 sum = make_float2(0.f, 0.f);
         const float2 c2 = make_float2(cr, cr), r2 = make_float2(-ref, -ref);
         __syncwarp();                                    // the stores take a converged warp
@@ -592,7 +599,7 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
       // O to the caller, through this item's query buffer (its products are complete);
       // pieces directly, [d / 4][row][4]
-      const float ms = m == neg_inf() ? m : m * c;       // log2 units
+      const float ms = m == neg_inf() ? m : row_ref(m, c, c);   // log2 units
       const long long piece = (long long)blockIdx.x * 2 + w.pslot;
       const int place = (split ? 0 : s * 128) + tl;
       float4* po = reinterpret_cast<float4*>(p.po) + piece * (p.d / 4) * UROWS + place;

@@ -122,3 +122,20 @@ def test_scores_of_any_size(n, hq, d, sign, dtype):
             assert (np.abs(out[b, i] - best_v) <= off * np.abs(best_v)).all(), (b, i)
             # base-2 and back: three roundings, and log2 e and ln 2 in fp32
             assert (np.abs(lse[b, i] - score[best]) <= 2.0 ** -21 * abs(score[best])).all(), (b, i)
+
+
+@pytest.mark.parametrize("d", [64, 128, 200])
+@pytest.mark.parametrize("n,hq", [(1, 8), (8, 64), (40, 32)])
+def test_large_values_of_a_token_that_raises_the_maximum(n, hq, d):
+    """bf16: V of 2^122 at a token whose score is e^5 times the others': no weight is above 1."""
+    c = _case(34, n=n, hq=hq, hkv=8, d=d, mask=None, ctx=(300,) * 24)
+    g, table, ctx = c[0], c[1], c[2]
+    g["q"].zero_()
+    g["q"][..., 0] = 1.0
+    g["k"][..., 0] = 0.0
+    for b in range(len(ctx)):
+        for t in (150, 290):
+            g["k"][_place(table, b, t)][:, 0] = 5.0
+        g["v"][_place(table, b, 150)][:, : d // 2] = 2.0 ** 122
+        g["v"][_place(table, b, 290)][:, d // 2:] = 2.0 ** 122
+    _check(_run(g, scale=1.0), *c, scale=1.0)
