@@ -633,8 +633,9 @@ class AttnOut:
 @functools.lru_cache(maxsize=1024)
 def _attn_workspace(shape, stride, code: int, max_pages: int, batch: int, n_stride: int,
                     heads_q: int, device: int) -> int:
-    return int(lib().tree_attention_workspace(_cache_desc(shape, stride, code, max_pages)[1], batch,
-                                              n_stride, heads_q))
+    ref = _cache_desc(shape, stride, code, max_pages)[1]
+    with torch.cuda.device(device):   # the pieces of the work follow that device's size
+        return int(lib().tree_attention_workspace(ref, batch, n_stride, heads_q))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -652,10 +653,11 @@ def _attn_plan(q_shape, q_stride, shape, stride, dtype, max_pages: int, device: 
 
 def tree_attention_workspace(k_cache: torch.Tensor, v_cache: torch.Tensor, max_pages: int,
                              batch: int, n_stride: int, heads_q: int) -> int:
-    """Workspace bytes tree_attention needs for these shapes on the current device."""
-    _cache(k_cache, v_cache, k_cache.device, max_pages)
+    """Workspace bytes tree_attention needs for these shapes on the caches' device."""
+    dev, _, _ = _on(k_cache, "k_cache", None)
+    _cache(k_cache, v_cache, dev, max_pages)
     return _attn_workspace(k_cache.shape, k_cache.stride(), _code(k_cache), max_pages, batch,
-                           n_stride, heads_q, torch.cuda.current_device())
+                           n_stride, heads_q, k_cache.get_device())
 
 
 def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
