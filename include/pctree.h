@@ -388,7 +388,9 @@ int32_t tree_verify_accept_noalloc(int32_t batch, int32_t n_stride, int32_t voca
  * PCT_EINVAL); head_dim is a multiple of 8 in 8..256. Offsets are 64-bit.
  * Block tables are [batch][max_pages] int32; entries past a request's pages are
  * never read. A request uses a page at most once, no two requests write the
- * same page, and the calls do not check that. Outputs do not overlap inputs.
+ * same page, and the calls do not check that. Outputs do not overlap inputs: of
+ * the dense arrays (lengths, counts, tables, slots, masks, paths, out, lse,
+ * status, workspace) that is checked (PCT_EINVAL), of q, new rows and caches not.
  * ------------------------------------------------------------------------ */
 typedef struct {
   int32_t n_pages;      /* pages of the cache, >= 1                                  */
@@ -504,7 +506,7 @@ int32_t tree_attention(const kv_cache_desc* desc, int32_t batch, int32_t n_strid
  * rises strictly. What lay behind the new length is unspecified afterwards.
  *   k_cache, v_cache: layer l at l * layer_stride elements (a multiple of 16 bytes)
  *   accept_path [batch][max_depth] int32
- *   new_len [batch] int64, not overlapping ctx_len
+ *   new_len [batch] int64, apart from ctx_len
  *   dev_status [batch]: PCT_DEV_BAD_COUNT (count below 1), PCT_DEV_BAD_LENGTH,
  *     PCT_DEV_BAD_PATH (accept_len outside 0..max_depth, or the path does not rise
  *     strictly within [1, count)), PCT_DEV_BAD_PAGE: the request's cache rows stay

@@ -1,6 +1,8 @@
 // C ABI of the paged cache and tree attention: argument checks and launches.
 // Like the rest of the ABI, nothing here synchronises or allocates.
+#include <algorithm>
 #include <cmath>
+#include <initializer_list>
 
 #include "internal.h"
 
@@ -40,6 +42,28 @@ int check_attn(const kv_cache_desc* d, int32_t batch, int32_t n, int32_t hq) {
   return PCT_OK;
 }
 
+// A call's dense array (null: not given). Blocks read lengths, counts, tables and paths at
+// different times and rely on reading the same values, so an output that overlaps one of
+// them would take indices and barriers out of step.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x && y && a.bytes && b.bytes && (x < y ? y - x < a.bytes : x - y < b.bytes);
+}
+// outputs apart from each other and from the inputs
+bool disjoint(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* a = outs.begin(); a != outs.end(); ++a) {
+    for (const Span* b = a + 1; b != outs.end(); ++b)
+      if (overlap(*a, *b)) return false;
+    for (const Span& b : ins)
+      if (overlap(*a, b)) return false;
+  }
+  return true;
+}
+
 #define PCT_CU(x)                             \
   do {                                        \
     if ((x) != cudaSuccess) return PCT_ECUDA; \
@@ -56,6 +80,11 @@ int32_t kv_pages_resize(int32_t batch, int32_t page_size, int32_t max_pages, int
   if (!batch_ok(batch) || !table_ok(page_size, max_pages, n_pages)) return PCT_EINVAL;
   if (!ctx_len || !block_table || !held || !free_pages || !free_count || !dev_status)
     return PCT_EINVAL;
+  const size_t nb = batch;
+  if (!disjoint({{block_table, nb * max_pages * 4}, {held, nb * 4}, {free_pages, (size_t)n_pages * 4},
+                 {free_count, 4}, {dev_status, nb * 4}},
+                {{ctx_len, nb * 8}, {count, nb * 4}}))
+    return PCT_EINVAL;
   if (!device_ok()) return PCT_EDEVICE;
   PCT_CU(launch_kv_pages_resize(batch, page_size, max_pages, n_pages, ctx_len, count, block_table,
                                 held, free_pages, free_count, dev_status,
@@ -71,6 +100,10 @@ int32_t kv_tree_slots(int32_t batch, int32_t n_stride, int32_t page_size, int32_
       !table_ok(page_size, max_pages, n_pages))
     return PCT_EINVAL;
   if (!ctx_len || !count || !block_table || !slot || !pos || !dev_status) return PCT_EINVAL;
+  const size_t nb = batch, rows = nb * n_stride;
+  if (!disjoint({{slot, rows * 8}, {pos, rows * 8}, {dev_status, nb * 4}},
+                {{ctx_len, nb * 8}, {count, nb * 4}, {depth, rows * 4}, {block_table, nb * max_pages * 4}}))
+    return PCT_EINVAL;
   if (!device_ok()) return PCT_EDEVICE;
   PCT_CU(launch_kv_tree_slots(batch, n_stride, page_size, max_pages, n_pages, ctx_len, count,
                               depth, block_table, slot, pos, dev_status,
@@ -91,6 +124,7 @@ int32_t kv_append(const kv_cache_desc* desc, int32_t batch, int32_t n_stride, co
     if (!stride_ok(new_stride[i], per)) return PCT_EINVAL;
   if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
     return PCT_EINVAL;
+  if (overlap({dev_status, (size_t)batch * 4}, {slot, (size_t)batch * n_stride * 8})) return PCT_EINVAL;
   if (!device_ok()) return PCT_EDEVICE;
   PCT_CU(launch_kv_append(*desc, batch, n_stride, k_new, v_new, new_stride, slot, k_cache, v_cache,
                           dev_status, static_cast<cudaStream_t>(cuda_stream)));
@@ -119,8 +153,14 @@ int32_t tree_attention(const kv_cache_desc* desc, int32_t batch, int32_t n_strid
     if (!stride_ok(q_stride[i], per)) return PCT_EINVAL;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
     return PCT_EINVAL;
-  if (!device_ok()) return PCT_EDEVICE;
+  const size_t nb = batch, rows = nb * n_stride;
   const size_t need = attn_workspace(*desc, batch, n_stride, heads_q);
+  if (!disjoint({{out, rows * heads_q * desc->head_dim * (desc->dtype == PCT_BF16 ? 2 : 4)},
+                 {lse, rows * heads_q * 4}, {dev_status, nb * 4}, {workspace, std::min(need, ws_bytes)}},
+                {{block_table, nb * desc->max_pages * 4}, {ctx_len, nb * 8}, {count, nb * 4},
+                 {mask, rows * ((n_stride + 31) / 32) * 4}}))
+    return PCT_EINVAL;
+  if (!device_ok()) return PCT_EDEVICE;
   if (!workspace || !aligned(workspace, 256) || ws_bytes < need) return PCT_EWORKSPACE;
   AttnArgs a;
   a.kv = *desc;
@@ -146,6 +186,11 @@ int32_t kv_commit(const kv_cache_desc* desc, int32_t batch, int32_t layers, int6
     return PCT_EINVAL;
   if (!stride_ok(layer_stride, desc->dtype == PCT_BF16 ? 8 : 4)) return PCT_EINVAL;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return PCT_EINVAL;
+  const size_t nb = batch;
+  if (!disjoint({{new_len, nb * 8}, {dev_status, nb * 4}},
+                {{block_table, nb * desc->max_pages * 4}, {ctx_len, nb * 8}, {count, nb * 4},
+                 {accept_len, nb * 4}, {accept_path, nb * max_depth * 4}}))
+    return PCT_EINVAL;
   if (!device_ok()) return PCT_EDEVICE;
   PCT_CU(launch_kv_commit(*desc, batch, layers, layer_stride, max_depth, k_cache, v_cache,
                           block_table, ctx_len, count, accept_len, accept_path, new_len,
