@@ -385,7 +385,9 @@ int32_t tree_verify_accept_noalloc(int32_t batch, int32_t n_stride, int32_t voca
  * with any strides (elements, innermost contiguous; the same for K and V), so
  * [n_pages][heads_kv][page_size][head_dim] and K and V interleaved by page work
  * too. Strides are multiples of 16 bytes, pointers 16-byte aligned (else
- * PCT_EINVAL); head_dim is a multiple of 8 in 8..256. Offsets are 64-bit.
+ * PCT_EINVAL); head_dim is a multiple of 8 in 8..256. Offsets are 64-bit. Rows
+ * may coincide (an axis of stride 0) where a cache is read; the calls that write
+ * ask for strides of head_dim at least on every axis of more than one entry.
  * Block tables are [batch][max_pages] int32; entries past a request's pages are
  * never read. A request uses a page at most once, no two requests write the
  * same page, and the calls do not check that. Outputs do not overlap inputs: of

@@ -29,6 +29,14 @@ int check_cache(const kv_cache_desc* d) {
     return PCT_EINVAL;
   return PCT_OK;
 }
+// For the calls that write: rows of a cache apart from each other. (An axis of stride 0, as an
+// expanded view has it, would be written by several blocks at once.)
+bool rows_apart(int64_t n, int64_t stride, int d) { return n == 1 || stride >= d; }
+bool writable(const kv_cache_desc& d) {
+  return rows_apart(d.n_pages, d.page_stride, d.head_dim) &&
+         rows_apart(d.page_size, d.slot_stride, d.head_dim) &&
+         rows_apart(d.heads_kv, d.head_stride, d.head_dim);
+}
 bool batch_ok(int32_t batch) { return batch >= 1 && batch <= 65535; }
 bool table_ok(int32_t page_size, int32_t max_pages, int32_t n_pages) {
   return page_size >= 1 && page_size <= 65536 && max_pages >= 1 && n_pages >= 1 &&
@@ -116,7 +124,7 @@ int32_t kv_append(const kv_cache_desc* desc, int32_t batch, int32_t n_stride, co
                   void* k_cache, void* v_cache, int32_t* dev_status, void* cuda_stream) {
   const int st = check_cache(desc);
   if (st != PCT_OK) return st;
-  if (!batch_ok(batch) || n_stride < 1 || n_stride > (1 << 20)) return PCT_EINVAL;
+  if (!batch_ok(batch) || n_stride < 1 || n_stride > (1 << 20) || !writable(*desc)) return PCT_EINVAL;
   if (!k_new || !v_new || !new_stride || !slot || !k_cache || !v_cache || !dev_status)
     return PCT_EINVAL;
   const int per = desc->dtype == PCT_BF16 ? 8 : 4;
@@ -185,6 +193,7 @@ int32_t kv_commit(const kv_cache_desc* desc, int32_t batch, int32_t layers, int6
       !new_len || !dev_status)
     return PCT_EINVAL;
   if (!stride_ok(layer_stride, desc->dtype == PCT_BF16 ? 8 : 4)) return PCT_EINVAL;
+  if (!writable(*desc) || !rows_apart(layers, layer_stride, desc->head_dim)) return PCT_EINVAL;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return PCT_EINVAL;
   const size_t nb = batch;
   if (!disjoint({{new_len, nb * 8}, {dev_status, nb * 4}},

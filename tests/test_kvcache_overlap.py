@@ -90,3 +90,36 @@ def test_attention_refusals_with_arguments_apart(bad):
                                         p(10 << 24), p(a["status"]), None, 0, None)
     assert call(base | bad) == pct.PCT_EINVAL
     assert call(base) in (pct.PCT_EWORKSPACE, 4)     # no workspace, or no device
+
+
+STRIDES = dict(page_stride=16 * 256, slot_stride=256, head_stride=64)
+
+
+@pytest.mark.parametrize("axis", ["page_stride", "slot_stride", "head_stride", "layer_stride"])
+@pytest.mark.parametrize("stride", [0, 56])
+def test_calls_that_write_refuse_rows_over_each_other(axis, stride):
+    """An expanded cache (stride 0) or rows closer than head_dim, where the axis has several entries."""
+    far = [ctypes.c_void_p((1 + i) << 28) for i in range(9)]
+    layers = 3
+
+    def calls(sizes, strides, layers, layer_stride):
+        d = ctypes.byref(pct.KvCacheDesc(sizes[0], sizes[1], WIDTH, sizes[2], 64, pct.PCT_BF16, *strides))
+        L = pct.lib()
+        yield "append", lambda: L.kv_append(d, B, N, far[0], far[1], STRIDE, far[2], far[3], far[4], far[5], None)
+        yield "commit", lambda: L.kv_commit(d, B, layers, layer_stride, DEPTH, *far, None)
+
+    sizes = [64, 16, 4]
+    strides = dict(STRIDES, layer_stride=64 * 16 * 256)
+    strides[axis] = stride
+    for name, call in calls(sizes, [strides[k] for k in STRIDES], layers, strides["layer_stride"]):
+        if axis != "layer_stride" or name == "commit":
+            assert call() == pct.PCT_EINVAL, name
+    if torch.cuda.is_available():                    # the next calls have nothing wrong but their pointers
+        pytest.skip("calls with made-up addresses pass the checks")
+    one = {"page_stride": 0, "slot_stride": 1, "head_stride": 2}
+    if axis in one:
+        sizes[one[axis]] = 1
+    else:
+        layers = 1
+    for name, call in calls(sizes, [strides[k] for k in STRIDES], layers, strides["layer_stride"]):
+        assert call() not in (pct.PCT_OK, pct.PCT_EINVAL), name
