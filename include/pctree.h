@@ -489,7 +489,7 @@ int32_t kv_append(const kv_cache_desc* desc, int32_t batch, int32_t n_stride, co
  * maxima, sums and the joins of a split axis are fp32. Results are the same from
  * call to call on the same device.
  * heads_q is a multiple of heads_kv, at most 64 times it; n_stride in 1..65536;
- * scale finite. The work is cut into equal parts over the device, along the cache
+ * |scale| below 2.35e38. The work is cut into equal parts over the device, along the cache
  * where rows are few, and joined by a second launch.
  * ------------------------------------------------------------------------ */
 size_t tree_attention_workspace(const kv_cache_desc* desc, int32_t batch, int32_t n_stride,

@@ -155,7 +155,7 @@ int32_t tree_attention(const kv_cache_desc* desc, int32_t batch, int32_t n_strid
   if (st != PCT_OK) return st;
   if (!q || !q_stride || !k_cache || !v_cache || !block_table || !ctx_len || !out || !dev_status)
     return PCT_EINVAL;
-  if (!std::isfinite(scale)) return PCT_EINVAL;
+  if (!std::isfinite(scale * 1.4426950f)) return PCT_EINVAL;   // the kernels' base-2 scale
   const int per = desc->dtype == PCT_BF16 ? 8 : 4;
   for (int i = 0; i < 3; ++i)
     if (!stride_ok(q_stride[i], per)) return PCT_EINVAL;

@@ -71,7 +71,7 @@ def test_overlapping_arrays_are_refused(name):
 
 
 BAD = [dict(batch=0), dict(batch=65536), dict(n=0), dict(n=65537), dict(hq=0), dict(hq=6), dict(hq=4 * 65),
-       dict(scale=float("nan")), dict(scale=float("inf")), dict(q=None), dict(st=None), dict(k=None), dict(v=None),
+       dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38), dict(scale=-2.4e38), dict(q=None), dict(st=None), dict(k=None), dict(v=None),
        dict(t=None), dict(c=None), dict(out=None), dict(status=None), dict(q=264), dict(k=264), dict(v=264),
        dict(out=264), dict(st=(4096, 100, 64)), dict(st=(-8, 256, 64))]
 
