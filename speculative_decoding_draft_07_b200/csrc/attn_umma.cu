@@ -457,8 +457,8 @@ attn_umma_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                            w.split ? w.mt * 2 * nodes : first, w.b);
           }
         }
-        if (!got) break;
         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        if (!got) break;                                 // (the group so far is waited for below)
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 #pragma unroll
         for (int s = 0; s < STREAMS; ++s) mbar_arrive(&qempty[s][buf]);
