@@ -473,7 +473,10 @@ int32_t kv_append(const kv_cache_desc* desc, int32_t batch, int32_t n_stride, co
  * A row that sees no token, and every row at i >= count[b], gives out = 0 and
  * lse = -inf. Cache places at or past token ctx_len + count, and nodes a row
  * does not see, do not enter its result whatever K holds there; V of the nodes
- * below count must be finite (0 * inf is NaN).
+ * below count must be finite (0 * inf is NaN). An infinite V that a row sees
+ * makes its element infinite. The sum of weights (1 for a row's best token) times
+ * values is fp32 before it is divided by the weights' sum, so |v| times the tokens
+ * that share a row has to stay below 3.4e38.
  *   q   [batch][n_stride][heads_q][head_dim] with strides q_stride (elements,
  *       {request, token, head}; multiples of 16 bytes), dtype of the cache
  *   out [batch][n_stride][heads_q][head_dim], dense, dtype of the cache

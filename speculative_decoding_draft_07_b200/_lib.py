@@ -671,7 +671,9 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     ctx_len [batch] int64, count [batch] int32 (None: n_stride for all), mask the words of
     tree_ancestor_mask [batch][n_stride][ceil(n_stride / 32)] int32 (None: a causal chain; a
     decode step with n_stride = 1). scale defaults to head_dim ** -0.5. Rows at or past count
-    are 0, their lse -inf. With out given, out.lse may be None."""
+    are 0, their lse -inf. bf16 inputs: the softmax's weights are rounded to bf16 for the product
+    with V (off by at most 2^-8 each; sums and lse are fp32); fp32 inputs are not rounded. With
+    out given, out.lse may be None. Outputs and workspace do not overlap inputs."""
     dev, s, ctx = _on(q, "q", stream)
     if q.dim() != 4:
         raise ValueError("q must be [batch][n_stride][heads_q][head_dim]")

@@ -5,9 +5,10 @@
 // accumulation: off by at most 5 * 2^-22 of |x y|, the size of an fp32 sum's own
 // rounding over twenty terms. On the FP32 pipes the same tiles took 2600 instructions a warp for 32 keys
 // x 32 rows and kept shared memory 60% busy (4 requests x 32 nodes, 8 heads of 64
-// over up to 1777 tokens: 40 us); this takes 27. Decode of 32 requests over up to 16384
-// tokens reads 4.4 TB/s (bound by the splitting, on the integer pipe); from some ten rows
-// on the products bound it.
+// over up to 1777 tokens: 40 us); this takes 28. Decode of 32 requests over up to 16384
+// tokens reads 4.5 TB/s: DRAM is at 50%, tensor pipe 39%, integer pipe 30%, issue 47%, so
+// nothing is full; with two warps a scheduler the chains of split and product wait for
+// themselves. From some ten rows on the products bound it.
 // The block is that of the bf16 kernel: four warps, WM of 16 rows each, the others
 // splitting a tile's keys, each with its own running maximum, sum and accumulator;
 // tiles of 64 keys (32 above head_dim 64) in a ring of asynchronous copies. Rows lie

@@ -4,7 +4,8 @@
 // larger ones whose pages (no multiple of 8 tokens), strides or scale (not positive)
 // the tcgen05 kernel cannot take. With so few rows against each key the cache's bytes
 // bound it and the warp-level matrix instructions keep up: 32 decode requests over up
-// to 32768 tokens, 8 heads of 128, 331 us (6.8 TB/s). A block of four
+// to 32768 tokens, 8 heads of 128, take 340-347 us on the device (6.5-6.6 TB/s; a copy, which
+// also writes, reaches 6.46). A block of four
 // warps is WM x WK: WM warps of 16 rows each, the others splitting the keys of a
 // tile (one row group: four warps on 16 keys each). Every warp keeps its own
 // running maximum, sum and 16 x head_dim accumulator in registers; they meet only

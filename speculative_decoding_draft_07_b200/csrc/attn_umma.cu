@@ -1,7 +1,7 @@
 // Tree attention for bf16 caches and many rows on the tcgen05 tensor cores.
 //
-// Above 64 rows (nodes x query heads of a group) the two products outweigh the
-// cache's bytes. One block an SM works on an item of two row tiles, R rows each
+// For calls of more than 32 rows (nodes x query heads of a group) a KV head: from some
+// 64 on the two products outweigh the cache's bytes. One block an SM works on an item of two row tiles, R rows each
 // (R = the largest multiple of the group up to 128), against key tiles of 64 tokens,
 // as two streams:
 //   * warp 0: TMA producer. Publishes the items, loads their queries (double
@@ -11,8 +11,8 @@
 //     (P from tensor memory) of stream 0 and 1. A stream's scores are double
 //     buffered, so its next S runs under the softmax of the current one. Two
 //     issuers because issuing blocks while products run and each change between
-//     the two kinds costs an issuer about 150 cycles: one thread for both streams
-//     takes 1768 cycles for 128 tokens of a stream, two threads 1269;
+//     the two kinds costs an issuer about 150 cycles: for a 64-token
+//     tile of both streams one thread takes 1768 cycles, two threads 1269;
 //   * warps 3-6 and 7-10: the softmax of stream 0 and 1. A thread reads its row of
 //     64 scores from tensor memory, keeps the running maximum and sum, and writes
 //     the weights back as bf16 over the scores. At an item's end they leave the
@@ -30,8 +30,8 @@
 // weights are taken relative to 2^8 times that one, so none is above 1.
 // 64 tokens a tile rather than 128: with 128 the scores fill tensor memory once
 // (head_dim 128), so that S, softmax and P V of a stream run one after another
-// (64 requests x 256 nodes over up to 4096 tokens: 1.41 ms; this takes 0.77-0.88,
-// 630-720 TFLOP/s). A 64-token tile of both streams takes about 2000 cycles, 1270 of
+// (64 requests x 256 nodes over up to 4096 tokens: 1.41 ms; this takes 0.75-0.93,
+// 600-740 TFLOP/s, by the clock that the power limit leaves). A 64-token tile of both streams takes about 2000 cycles, 1270 of
 // products alone and 1024 of exponentials, which overlap in part.
 // Every mbarrier wait is bounded; when one gives up, the roles run to the end
 // without waiting, drain their copies and products, free the tensor memory, and

@@ -227,7 +227,7 @@ cudaError_t launch_kv_commit(const kv_cache_desc& d, int batch, int layers, int6
                              const int32_t* accept_path, int64_t* new_len, int32_t* status,
                              cudaStream_t s);
 
-// ---- tree attention (tree_attn*.cu) -------------------------------------------
+// ---- tree attention (tree_attn.cu, attn_*.cu) -------------------------------------------
 struct AttnArgs {
   kv_cache_desc kv;
   int batch, n, hq;             // n = n_stride
