@@ -123,3 +123,51 @@ def test_calls_that_write_refuse_rows_over_each_other(axis, stride):
         layers = 1
     for name, call in calls(sizes, [strides[k] for k in STRIDES], layers, strides["layer_stride"]):
         assert call() not in (pct.PCT_OK, pct.PCT_EINVAL), name
+
+
+def _apart(n):
+    return [ctypes.c_void_p((1 + i) << 28) for i in range(n)]
+
+
+CALLS = {
+    "kv_append": (dict(d=DESC, batch=2, n=4, st=(4096, 256, 64), p=6),
+                  [dict(batch=0), dict(batch=65536), dict(n=0), dict(n=(1 << 20) + 1), dict(st=(4096, 4, 64)), dict(st=(-8, 256, 64)),
+                   dict(st=None), dict(odd=0), dict(odd=1), dict(odd=3), dict(odd=4)] + [dict(null=i) for i in range(6)]),
+    "kv_commit": (dict(d=DESC, batch=2, layers=1, ls=0, depth=4, p=9),
+                  [dict(batch=0), dict(batch=65536), dict(layers=0), dict(layers=65536), dict(ls=4), dict(ls=-8), dict(depth=0),
+                   dict(depth=4097), dict(odd=0), dict(odd=1)] + [dict(null=i) for i in range(9)]),
+    "kv_pages_resize": (dict(batch=2, page=16, width=8, n_pages=10, p=7),
+                        [dict(batch=0), dict(batch=65536), dict(page=0), dict(page=65537), dict(width=0), dict(n_pages=0),
+                         dict(page=65536, width=16385)] + [dict(null=i) for i in (0, 2, 3, 4, 5, 6)]),
+    "kv_tree_slots": (dict(batch=2, n=4, page=16, width=8, n_pages=10, p=7),
+                      [dict(batch=0), dict(batch=65536), dict(n=0), dict(n=(1 << 20) + 1), dict(page=0), dict(page=65537),
+                       dict(width=0), dict(n_pages=0), dict(page=65536, width=16385)] + [dict(null=i) for i in (0, 1, 3, 4, 5, 6)]),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_refusals_with_arguments_apart(name):
+    """Each refusal of the other calls by itself: nothing else is wrong with the call."""
+    base, bad = CALLS[name]
+    L = pct.lib()
+
+    def call(a):
+        p = _apart(a["p"])
+        if "null" in a:
+            p[a["null"]] = None
+        if "odd" in a:
+            p[a["odd"]] = ctypes.c_void_p(p[a["odd"]].value + 8)
+        if name == "kv_append":
+            st = None if a["st"] is None else (ctypes.c_int64 * 3)(*a["st"])
+            return L.kv_append(ctypes.byref(a["d"]), a["batch"], a["n"], p[0], p[1], st, p[2], p[3], p[4], p[5], None)
+        if name == "kv_commit":
+            return L.kv_commit(ctypes.byref(a["d"]), a["batch"], a["layers"], a["ls"], a["depth"], *p, None)
+        if name == "kv_pages_resize":
+            return L.kv_pages_resize(a["batch"], a["page"], a["width"], a["n_pages"], *p, None)
+        return L.kv_tree_slots(a["batch"], a["n"], a["page"], a["width"], a["n_pages"], *p, None)
+
+    for b in bad:
+        assert call(base | b) == pct.PCT_EINVAL, b
+    if torch.cuda.is_available():                    # the next call has nothing wrong but its pointers
+        pytest.skip("calls with made-up addresses pass the checks")
+    assert call(base) not in (pct.PCT_OK, pct.PCT_EINVAL)
